@@ -16,7 +16,8 @@
  *     (i / W, i % W). An offset is query minus key, (dr, dc) = (r_i - r_j,
  *     c_i - c_j).
  *   - Device pointers must be 16-byte aligned and point to contiguous
- *     row-major memory of the stated shape. The caller owns every buffer;
+ *     row-major memory of the stated shape (the calls on tokens, which take
+ *     an rpe_view, state their own rules). The caller owns every buffer;
  *     the library never frees or keeps a caller pointer after the call.
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*;
  *     NULL = the legacy default stream). Argument errors are detected on the
@@ -77,6 +78,10 @@ enum { RPE_CLS_TOKEN = 32 };
 
 /* Element types of q, k, v, out and the iRPE tables. */
 enum { RPE_DTYPE_BF16 = 0, RPE_DTYPE_F32 = 1 };
+
+/* fp16, taken by the calls on tokens (rope_fwd, qk_norm_rope_fwd,
+ * packed_attn_fwd) only. */
+enum { RPE_DTYPE_F16 = 2 };
 
 /*
  * rpe_build_bucket_ids -- iRPE eq. 18 with the eq. 25 (Product) or the
@@ -316,6 +321,102 @@ int swin_noalloc_status_word(unsigned **word);
 int swin_window_attn_fwd_fmap(const void *q, const void *k, const void *v,
                               const float *bias_table, int batch, int img_h, int img_w,
                               int heads, int M, int d, void *out, void *stream);
+
+/*
+ * rpe_view -- a [batch, tokens, heads, d] tensor with strides, counted in
+ * elements; the d channels of a head are contiguous. It describes a part of a
+ * projection's output [tokens, heads_q + 2 heads_k, d] as well as the
+ * [B, heads, N, d] tensors of the grid calls. Strides must not be negative;
+ * the stride of an axis with one entry is not read.
+ */
+typedef struct rpe_view {
+    void *data;
+    int64_t batch_stride, token_stride, head_stride;
+} rpe_view;
+
+/* Scaled frequencies of rope_build_phases. */
+enum {
+    RPE_ROPE_NONE = 0,
+    RPE_ROPE_LINEAR = 1, /* f / factor                                          */
+    RPE_ROPE_NTK = 2,    /* base * factor^(D / (D - 2))                         */
+    RPE_ROPE_BANDS = 3,  /* f / factor below `low` turns over the context, f
+                            above `high`, blended by the turns in between       */
+    RPE_ROPE_YARN = 4    /* the same blend by the pair's index, and a magnitude
+                            of 0.1 ln(factor) + 1                               */
+};
+/* Flags of rope_fwd and qk_norm_rope_fwd: pairs (x[2p], x[2p + 1]) instead of
+ * (x[p], x[p + rotary_dim / 2]); turned back (rope_fwd only: the inverse for
+ * magnitude 1, and for any magnitude the gradient of the turn); positions
+ * [batch, tokens, axes] instead of [tokens, axes] shared by the batch. */
+enum { RPE_ROPE_INTERLEAVED = 1, RPE_ROPE_INVERSE = 2, RPE_ROPE_BATCH_POSITIONS = 4 };
+/* Norms of qk_norm_rope_fwd. */
+enum { RPE_NORM_RMS = 0, RPE_NORM_LAYER = 1 };
+
+/*
+ * rope_build_phases -- the table of phases that the rotary calls read.
+ *
+ * The rotary_dim / 2 pairs of a head are dealt to `axes` axes (1: a line; 2:
+ * the rows, then the columns of a patch grid), D = rotary_dim / axes channels
+ * each. Pair i of an axis turns by f_i = base^(-2 i / D) radians per position,
+ * changed as `scaling` says. phases (device, rotary_dim / 2 of 64 bits) holds
+ * f / 2 pi in units of 2^-64 turns: the low 64 bits of position * phase are
+ * the angle's fraction of a turn, exact for every 32-bit position.
+ * factor >= 1 (not read for RPE_ROPE_NONE); context > 0 tokens and
+ * 0 < low < high turns (BANDS and YARN). YARN ramps over the pair index from
+ * the pair that turns `high` times over the context (kept) to the one that
+ * turns `low` times (divided by factor).
+ * *magnitude (host) is what the rotary calls take as `magnitude`: 1 but for
+ * YARN. Errors: RPE_ERR_INVALID_ARG for a value outside the above, base <= 1,
+ * rotary_dim not a multiple of 2 axes; RPE_ERR_UNSUPPORTED for
+ * rotary_dim > 256.
+ */
+int rope_build_phases(int rotary_dim, int axes, int scaling, double base, double factor,
+                      double context, double low, double high, uint64_t *phases,
+                      float *magnitude, void *stream);
+
+/*
+ * rope_fwd -- turns the first rotary_dim channels of each head of q and k by
+ * their token's position and writes the whole heads:
+ *
+ *   (y1, y2) = magnitude (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ *   a = position[axis of the pair] * f[pair]
+ *
+ * in 32 bits, rounded once; the other channels are copied.
+ * q, q_out     : [batch, tokens, heads_q, d] views, element type `dtype`
+ *                (bf16, fp16 or fp32), any strides and element-aligned
+ *                pointers (16-byte vectors are used where they fit).
+ * k, k_out     : the same with heads_k heads; heads_k == 0: not read.
+ * An output may be its input (turned in place); otherwise no output overlaps
+ * an input or the other output.
+ * positions    : device int32 [tokens, axes] (or [batch, tokens, axes], see
+ *                RPE_ROPE_BATCH_POSITIONS), any values.
+ * phases       : device table of rope_build_phases for this rotary_dim and axes.
+ * Supported: d <= 256, any even rotary_dim in [2, d] that 2 axes divides,
+ * batch * tokens < 2^31 (zero: RPE_OK, nothing is done), heads <= 65536.
+ */
+int rope_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *q_out, const rpe_view *k_out,
+             const int32_t *positions, int axes, const uint64_t *phases, int rotary_dim,
+             float magnitude, unsigned flags, int64_t batch, int64_t tokens, int heads_q,
+             int heads_k, int d, int dtype, void *stream);
+
+/*
+ * qk_norm_rope_fwd -- each head of q and k normed, then turned as rope_fwd
+ * does, in one pass:
+ *
+ *   RPE_NORM_RMS:   y = x / sqrt(mean(x^2) + eps) * gain
+ *   RPE_NORM_LAYER: y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * gain
+ *
+ * over the d channels of a head, in 32 bits, rounded once after the rotation.
+ * gain_q, gain_k: device [d], of `dtype` or fp32 as gain_dtype says; NULL: ones.
+ * rotary_dim may be 0 (norms alone; positions and phases are not read).
+ * Everything else as for rope_fwd, without RPE_ROPE_INVERSE.
+ */
+int qk_norm_rope_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *q_out,
+                     const rpe_view *k_out, int norm, float eps, const void *gain_q,
+                     const void *gain_k, int gain_dtype, const int32_t *positions, int axes,
+                     const uint64_t *phases, int rotary_dim, float magnitude, unsigned flags,
+                     int64_t batch, int64_t tokens, int heads_q, int heads_k, int d, int dtype,
+                     void *stream);
 
 /*
  * rpe_device_status -- synchronises the current device and returns, through

@@ -24,9 +24,20 @@ RPE_TERM_K, RPE_TERM_Q, RPE_TERM_V = 1, 2, 4
 RPE_TABLES_CROSS = 8
 RPE_TABLES_PER_HEAD = 16
 RPE_CLS_TOKEN = 32
-RPE_DTYPE_BF16, RPE_DTYPE_F32 = 0, 1
+RPE_DTYPE_BF16, RPE_DTYPE_F32, RPE_DTYPE_F16 = 0, 1, 2
+RPE_ROPE_NONE, RPE_ROPE_LINEAR, RPE_ROPE_NTK, RPE_ROPE_BANDS, RPE_ROPE_YARN = 0, 1, 2, 3, 4
+RPE_ROPE_INTERLEAVED, RPE_ROPE_INVERSE, RPE_ROPE_BATCH_POSITIONS = 1, 2, 4
+RPE_NORM_RMS, RPE_NORM_LAYER = 0, 1
+
+
+class View(ctypes.Structure):
+    """rpe_view: a [batch, tokens, heads, d] tensor with element strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
 
 # name -> (restype, argtypes) for every symbol the header declares
+_f, _i64, _view = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(View)
 _i, _u, _d, _p, _u64 = ctypes.c_int, ctypes.c_uint, ctypes.c_double, ctypes.c_void_p, ctypes.c_uint64
 SIGNATURES = {
     "rpe_build_bucket_ids": (_i, [_i, _i, _i, _d, _d, _d, _p, _p, ctypes.POINTER(_i), _p]),
@@ -38,6 +49,11 @@ SIGNATURES = {
     "swin_window_attn_fwd_fmap": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _p]),
     "rpe_attn_bias_fwd": (_i, [_p, _p, _p, _p, _i, _p, _i, ctypes.c_uint, _i, _i, _i, _i, _i, _i,
                                _p, _p]),
+    "rope_build_phases": (_i, [_i, _i, _i, _d, _d, _d, _d, _d, _p, ctypes.POINTER(_f), _p]),
+    "rope_fwd": (_i, [_view, _view, _view, _view, _p, _i, _p, _i, _f, _u, _i64, _i64, _i, _i, _i,
+                      _i, _p]),
+    "qk_norm_rope_fwd": (_i, [_view, _view, _view, _view, _i, _f, _p, _p, _i, _p, _i, _p, _i, _f,
+                              _u, _i64, _i64, _i, _i, _i, _i, _p]),
     "rpe_device_status": (_i, [ctypes.POINTER(_u), _i]),
     "rpe_wait_probe": (_i, [_u64, _p]),
     "rpe_status_string": (ctypes.c_char_p, [_i]),

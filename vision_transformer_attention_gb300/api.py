@@ -13,6 +13,8 @@ from . import _lib
 from ._lib import check
 
 _DTYPES = {torch.bfloat16: _lib.RPE_DTYPE_BF16, torch.float32: _lib.RPE_DTYPE_F32}
+# the calls on tokens take fp16 too
+_TOKEN_DTYPES = {**_DTYPES, torch.float16: _lib.RPE_DTYPE_F16}
 
 
 def _stream(t):
@@ -177,6 +179,125 @@ def swin_window_attn_fwd_fmap(q, k, v, bias_table, M, out=None):
             _ptr(q), _ptr(k), _ptr(v), _ptr(bias_table), batch, img_h, img_w, heads, M, d,
             _ptr(out), _stream(q)))
     return out
+
+
+def _view(t, name, dtype=None, shape=None, device=None):
+    """rpe_view of a [tokens, heads, d] or [batch, tokens, heads, d] tensor with any
+    strides whose channels are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [tokens, heads, d] or [batch, tokens, heads, d]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    strides = t.stride() if t.dim() == 4 else (0, *t.stride())
+    return _lib.View(t.data_ptr(), *strides[:3])
+
+
+def rope_build_phases(rotary_dim, axes=1, base=10000.0, scaling=_lib.RPE_ROPE_NONE, factor=1.0,
+                      context=0, low=1.0, high=32.0, device="cuda"):
+    """Phase table of the rotary calls: rotary_dim / 2 pairs dealt to `axes` axes (1: a line,
+    2: the rows and columns of a patch grid), frequencies base^(-2i/D) scaled as RPE_ROPE_*
+    says. Returns (phases int64 [rotary_dim / 2], in 2^-64 turns per position, magnitude)."""
+    device = torch.device(device)
+    phases = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.int64, device=device)
+    magnitude = ctypes.c_float(0)
+    with torch.cuda.device(device):
+        check("rope_build_phases", _lib.lib().rope_build_phases(
+            rotary_dim, axes, scaling, float(base), float(factor), float(context), float(low),
+            float(high), _ptr(phases), ctypes.byref(magnitude), _stream(phases)))
+    return phases, magnitude.value
+
+
+def _rope_args(q, k, positions, phases, interleaved, magnitude, q_out, k_out):
+    """What rope_fwd and qk_norm_rope_fwd share: the outputs, the four views and the
+    arguments from the positions on."""
+    qv = _view(q, "q")
+    if q.dtype not in _TOKEN_DTYPES:
+        raise TypeError("q must be bfloat16, float16 or float32")
+    lead, (heads_q, d) = tuple(q.shape[:-2]), q.shape[-2:]
+    kv = None if k is None else _view(k, "k", q.dtype, device=q.device)
+    heads_k = 0 if k is None else k.shape[-2]
+    if k is not None and tuple(k.shape) != (*lead, heads_k, d):
+        raise ValueError(f"k must be {(*lead, 'heads', d)}, got {tuple(k.shape)}")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    qo = _view(q_out, "q_out", q.dtype, q.shape, q.device)
+    if k is None:
+        k_out, ko = None, None
+    else:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        ko = _view(k_out, "k_out", k.dtype, k.shape, k.device)
+    batch, tokens = lead if len(lead) == 2 else (1, lead[0])
+    flags = _lib.RPE_ROPE_INTERLEAVED if interleaved else 0
+    axes, rotary_dim = 1, 0
+    if phases is not None:
+        _need(phases, "phases", torch.int64, device=q.device)
+        rotary_dim = 2 * phases.numel()
+        _need(positions, "positions", torch.int32, device=q.device)
+        shape = tuple(positions.shape)
+        if len(lead) == 2 and len(shape) == 3 and shape[:2] == lead and shape[2] in (1, 2):
+            axes = shape[2]
+            flags |= _lib.RPE_ROPE_BATCH_POSITIONS
+        elif shape in ((tokens,), (tokens, 1), (tokens, 2)):
+            axes = shape[1] if len(shape) == 2 else 1
+        else:
+            raise ValueError(f"positions must be [tokens], [tokens, axes] or [batch, tokens, axes] "
+                             f"with {tokens} tokens; got {shape}")
+    ref = lambda v: None if v is None else ctypes.byref(v)  # noqa: E731
+    views = (ref(qv), ref(kv), ref(qo), ref(ko))
+    rest = lambda extra: (  # noqa: E731
+        _ptr(positions) if rotary_dim else None, axes, _ptr(phases) if rotary_dim else None,
+        rotary_dim, float(magnitude), flags | extra, batch, tokens, heads_q, heads_k, d,
+        _TOKEN_DTYPES[q.dtype], _stream(q))
+    return q_out, k_out, views, rest
+
+
+def rope_fwd(q, k, positions, phases, interleaved=False, inverse=False, magnitude=1.0, q_out=None,
+             k_out=None):
+    """Rotary positions on q [tokens, heads, d] or [batch, tokens, heads, d] and k (None, or
+    the same with its own heads), any strides with contiguous channels: the first
+    2 * len(phases) channels of each head turned, the others copied. positions: int32
+    [tokens] or [tokens, axes], shared by the batch, or [batch, tokens, axes]. q_out and
+    k_out may be q and k. Returns (q_out, k_out or None)."""
+    if phases is None:
+        raise ValueError("phases must be a table of rope_build_phases")
+    q_out, k_out, views, rest = _rope_args(q, k, positions, phases, interleaved, magnitude, q_out,
+                                           k_out)
+    with torch.cuda.device(q.device):
+        check("rope_fwd", _lib.lib().rope_fwd(
+            *views, *rest(_lib.RPE_ROPE_INVERSE if inverse else 0)))
+    return q_out, k_out
+
+
+def qk_norm_rope_fwd(q, k, q_gain, k_gain, positions=None, phases=None, norm=_lib.RPE_NORM_RMS,
+                     eps=1e-6, interleaved=False, magnitude=1.0, q_out=None, k_out=None):
+    """The norm of each head of q and k (RPE_NORM_RMS or RPE_NORM_LAYER, gains [d] of q's
+    type or float32, None: ones) and the rotation of rope_fwd (phases None: no rotation) in
+    one pass. Returns (q_out, k_out or None)."""
+    q_out, k_out, views, rest = _rope_args(q, k, positions, phases, interleaved, magnitude, q_out,
+                                           k_out)
+    gains = [g for g in (q_gain, k_gain) if g is not None]
+    gain_dtype = gains[0].dtype if gains else q.dtype
+    if gain_dtype not in (q.dtype, torch.float32):
+        raise TypeError(f"gains must have dtype {q.dtype} or float32")
+    for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if g is not None:
+            _need(g, name, gain_dtype, (q.shape[-1],), q.device)
+    with torch.cuda.device(q.device):
+        check("qk_norm_rope_fwd", _lib.lib().qk_norm_rope_fwd(
+            *views[:4], norm, float(eps), _ptr(q_gain), _ptr(k_gain), _TOKEN_DTYPES[gain_dtype],
+            *rest(0)))
+    return q_out, k_out
 
 
 def rpe_device_status(clear=True):

@@ -138,6 +138,31 @@ bool launch_rpe_bf16_pingpong(const RpeBf16Args &a, cudaStream_t stream, cudaErr
 // an offset table whose ids form one run per grid row of keys).
 bool launch_rpe_bf16_pingpong_qv(const RpeBf16Args &a, cudaStream_t stream, cudaError_t *err);
 
+// Rotary positions (and per-head norms) of queries (role 0) and keys (role 1).
+// Views are [batch, tokens, heads, d] with element strides.
+struct RopeView {
+    void *data;
+    int64_t batch_stride, token_stride, head_stride;
+};
+struct RopeArgs {
+    RopeView src[2], dst[2];  // may be the same memory (turned in place)
+    int heads[2];             // 0: the role is absent
+    int64_t units, tokens;    // batch * tokens, tokens per batch
+    int d, rotary, axes, axis_pairs;  // pairs per axis (rotary / 2 / axes)
+    const int32_t *positions;         // [tokens, axes], or [batch, tokens, axes]
+    int64_t pos_batch;                // tokens between batches' positions (0: shared)
+    const uint64_t *phases;           // [rotary / 2], 2^-64 turns per position
+    float magnitude;
+    int inverse, interleaved;
+    int norm, layer, gain_f32;  // norm each head first; by its variance; gains in fp32
+    const void *gain[2];        // [d], or NULL
+    float eps;
+    int lanes, wpt;  // set by the launcher: lanes per head, warps per token
+};
+cudaError_t launch_rope_bf16(const RopeArgs &a, cudaStream_t stream);
+cudaError_t launch_rope_f16(const RopeArgs &a, cudaStream_t stream);
+cudaError_t launch_rope_f32(const RopeArgs &a, cudaStream_t stream);
+
 cudaError_t launch_wait_probe(unsigned long long limit_ns, cudaStream_t stream);
 
 }  // namespace vta
