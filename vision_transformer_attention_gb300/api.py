@@ -181,6 +181,21 @@ def swin_window_attn_fwd_fmap(q, k, v, bias_table, M, out=None):
     return out
 
 
+def _call(t, name, *args):
+    """Calls the entry point with t's device current and that device's current stream as the
+    last argument. (The device guard and the stream object cost as much as a small kernel, so
+    the guard is entered only where the device differs.)"""
+    fn = getattr(_lib.lib(), name)
+    device = t.get_device()
+    if device == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    if rc != _lib.RPE_OK:
+        raise _lib.RpeError(name, rc)
+
+
 def _view(t, name, dtype=None, shape=None, device=None):
     """rpe_view of a [tokens, heads, d] or [batch, tokens, heads, d] tensor with any
     strides whose channels are contiguous."""
@@ -190,16 +205,20 @@ def _view(t, name, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if t.dim() not in (3, 4):
+    strides = t.stride()
+    if len(strides) == 4:
+        b, n, h, c = strides
+    elif len(strides) == 3:
+        b, (n, h, c) = 0, strides
+    else:
         raise ValueError(f"{name} must be [tokens, heads, d] or [batch, tokens, heads, d]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if c != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have contiguous channels")
-    strides = t.stride() if t.dim() == 4 else (0, *t.stride())
-    return _lib.View(t.data_ptr(), *strides[:3])
+    return _lib.View(t.data_ptr(), b, n, h)
 
 
 def rope_build_phases(rotary_dim, axes=1, base=10000.0, scaling=_lib.RPE_ROPE_NONE, factor=1.0,
@@ -217,49 +236,48 @@ def rope_build_phases(rotary_dim, axes=1, base=10000.0, scaling=_lib.RPE_ROPE_NO
     return phases, magnitude.value
 
 
-def _rope_args(q, k, positions, phases, interleaved, magnitude, q_out, k_out):
+def _rope_args(q, k, positions, phases, interleaved, inverse, magnitude, q_out, k_out):
     """What rope_fwd and qk_norm_rope_fwd share: the outputs, the four views and the
     arguments from the positions on."""
     qv = _view(q, "q")
-    if q.dtype not in _TOKEN_DTYPES:
+    dtype, device, shape = q.dtype, q.device, q.shape
+    code = _TOKEN_DTYPES.get(dtype)
+    if code is None:
         raise TypeError("q must be bfloat16, float16 or float32")
-    lead, (heads_q, d) = tuple(q.shape[:-2]), q.shape[-2:]
-    kv = None if k is None else _view(k, "k", q.dtype, device=q.device)
-    heads_k = 0 if k is None else k.shape[-2]
-    if k is not None and tuple(k.shape) != (*lead, heads_k, d):
-        raise ValueError(f"k must be {(*lead, 'heads', d)}, got {tuple(k.shape)}")
+    batch, tokens, heads_q, d = shape if len(shape) == 4 else (1, *shape)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    qo = _view(q_out, "q_out", q.dtype, q.shape, q.device)
-    if k is None:
-        k_out, ko = None, None
-    else:
+        q_out = torch.empty(shape, dtype=dtype, device=device)
+    qo = _view(q_out, "q_out", dtype, shape, device)
+    kv = ko = None
+    heads_k = 0
+    if k is not None:
+        kv = _view(k, "k", dtype, None, device)
+        heads_k = k.shape[-2]
+        if k.shape != (*shape[:-2], heads_k, d):
+            raise ValueError(f"k must be {(*shape[:-2], 'heads', d)}, got {tuple(k.shape)}")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        ko = _view(k_out, "k_out", k.dtype, k.shape, k.device)
-    batch, tokens = lead if len(lead) == 2 else (1, lead[0])
-    flags = _lib.RPE_ROPE_INTERLEAVED if interleaved else 0
-    axes, rotary_dim = 1, 0
+            k_out = torch.empty(k.shape, dtype=dtype, device=device)
+        ko = _view(k_out, "k_out", dtype, k.shape, device)
+    flags = (_lib.RPE_ROPE_INTERLEAVED if interleaved else 0) | (
+        _lib.RPE_ROPE_INVERSE if inverse else 0)
+    axes, rotary_dim, pos_ptr, phase_ptr = 1, 0, None, None
     if phases is not None:
-        _need(phases, "phases", torch.int64, device=q.device)
+        _need(phases, "phases", torch.int64, device=device)
+        _need(positions, "positions", torch.int32, device=device)
         rotary_dim = 2 * phases.numel()
-        _need(positions, "positions", torch.int32, device=q.device)
-        shape = tuple(positions.shape)
-        if len(lead) == 2 and len(shape) == 3 and shape[:2] == lead and shape[2] in (1, 2):
-            axes = shape[2]
+        pos_ptr, phase_ptr = positions.data_ptr(), phases.data_ptr()
+        pshape = tuple(positions.shape)
+        if len(pshape) == 3 and pshape[:2] == tuple(shape[:-2]) and pshape[2] in (1, 2):
+            axes = pshape[2]
             flags |= _lib.RPE_ROPE_BATCH_POSITIONS
-        elif shape in ((tokens,), (tokens, 1), (tokens, 2)):
-            axes = shape[1] if len(shape) == 2 else 1
+        elif pshape in ((tokens,), (tokens, 1), (tokens, 2)):
+            axes = pshape[1] if len(pshape) == 2 else 1
         else:
             raise ValueError(f"positions must be [tokens], [tokens, axes] or [batch, tokens, axes] "
-                             f"with {tokens} tokens; got {shape}")
-    ref = lambda v: None if v is None else ctypes.byref(v)  # noqa: E731
-    views = (ref(qv), ref(kv), ref(qo), ref(ko))
-    rest = lambda extra: (  # noqa: E731
-        _ptr(positions) if rotary_dim else None, axes, _ptr(phases) if rotary_dim else None,
-        rotary_dim, float(magnitude), flags | extra, batch, tokens, heads_q, heads_k, d,
-        _TOKEN_DTYPES[q.dtype], _stream(q))
-    return q_out, k_out, views, rest
+                             f"with {tokens} tokens; got {pshape}")
+    rest = (pos_ptr, axes, phase_ptr, rotary_dim, magnitude, flags, batch, tokens, heads_q,
+            heads_k, d, code)
+    return q_out, k_out if k is not None else None, (qv, kv, qo, ko), rest
 
 
 def rope_fwd(q, k, positions, phases, interleaved=False, inverse=False, magnitude=1.0, q_out=None,
@@ -271,11 +289,9 @@ def rope_fwd(q, k, positions, phases, interleaved=False, inverse=False, magnitud
     k_out may be q and k. Returns (q_out, k_out or None)."""
     if phases is None:
         raise ValueError("phases must be a table of rope_build_phases")
-    q_out, k_out, views, rest = _rope_args(q, k, positions, phases, interleaved, magnitude, q_out,
-                                           k_out)
-    with torch.cuda.device(q.device):
-        check("rope_fwd", _lib.lib().rope_fwd(
-            *views, *rest(_lib.RPE_ROPE_INVERSE if inverse else 0)))
+    q_out, k_out, views, rest = _rope_args(q, k, positions, phases, interleaved, inverse,
+                                           magnitude, q_out, k_out)
+    _call(q, "rope_fwd", *views, *rest)
     return q_out, k_out
 
 
@@ -284,19 +300,17 @@ def qk_norm_rope_fwd(q, k, q_gain, k_gain, positions=None, phases=None, norm=_li
     """The norm of each head of q and k (RPE_NORM_RMS or RPE_NORM_LAYER, gains [d] of q's
     type or float32, None: ones) and the rotation of rope_fwd (phases None: no rotation) in
     one pass. Returns (q_out, k_out or None)."""
-    q_out, k_out, views, rest = _rope_args(q, k, positions, phases, interleaved, magnitude, q_out,
-                                           k_out)
-    gains = [g for g in (q_gain, k_gain) if g is not None]
-    gain_dtype = gains[0].dtype if gains else q.dtype
-    if gain_dtype not in (q.dtype, torch.float32):
-        raise TypeError(f"gains must have dtype {q.dtype} or float32")
-    for name, g in (("q_gain", q_gain), ("k_gain", k_gain)):
+    q_out, k_out, views, rest = _rope_args(q, k, positions, phases, interleaved, False,
+                                           magnitude, q_out, k_out)
+    gain_dtype, ptrs = None, [None, None]
+    for i, g in enumerate((q_gain, k_gain)):
         if g is not None:
+            name = "k_gain" if i else "q_gain"
+            gain_dtype = gain_dtype or (torch.float32 if g.dtype == torch.float32 else q.dtype)
             _need(g, name, gain_dtype, (q.shape[-1],), q.device)
-    with torch.cuda.device(q.device):
-        check("qk_norm_rope_fwd", _lib.lib().qk_norm_rope_fwd(
-            *views[:4], norm, float(eps), _ptr(q_gain), _ptr(k_gain), _TOKEN_DTYPES[gain_dtype],
-            *rest(0)))
+            ptrs[i] = g.data_ptr()
+    _call(q, "qk_norm_rope_fwd", *views, norm, eps, *ptrs, _TOKEN_DTYPES[gain_dtype or q.dtype],
+          *rest)
     return q_out, k_out
 
 

@@ -16,14 +16,24 @@
 // and a range reduction. Its top 32 bits, as a signed fraction of a half turn,
 // go to sincospif.
 //
-// Bound: every element is read and written once (memory). A lane holds the
-// same 8 (16-bit types) or 4 (32-bit) pairs of each head it visits, so the
-// angles of a token are formed once per warp and used for all of its heads;
-// L lanes cover one head, 32 / L heads are in flight per warp, and a head's
-// norm is a butterfly over its L lanes. Loads are V elements wide, the widest
-// width that the pair layout, the strides and the pointers allow. A token's
-// heads are dealt over `wpt` warps where there are too few tokens to fill the
-// GPU.
+// Bound: every element is read and written once (memory). Two kernels:
+//
+//   rope_wide_kernel, where everything can move in 16-byte vectors. Persistent
+//   warps walk over (token, pass) items, a pass being 32 / L heads of one role:
+//   L lanes take a head, each lane two vectors. The vectors of the next
+//   kRopeStages - 1 passes are on their way into a shared-memory ring
+//   (cp.async, each lane reads back only what it asked for, so no barrier);
+//   with loads into registers a warp had one pass in flight and reached 2.4
+//   to 4.2 TB/s. A token's cosines and sines are formed once, by the lanes
+//   together, and stay in registers for all of its heads. A head's norm is a
+//   butterfly over its L lanes, and the arithmetic runs on pairs of floats
+//   (one instruction for two).
+//
+//   rope_any_kernel, for every other stride, alignment and pair count: the
+//   same split, element by element, V at a time, no ring.
+//
+// Where there are too few tokens to fill the GPU a token's passes are dealt
+// over `wpt` warps.
 #pragma once
 #include "vta_internal.h"
 #include "sm103_ptx.cuh"
@@ -31,7 +41,9 @@
 namespace vta {
 namespace {
 
-constexpr int kRopeWarps = 4;  // warps per CTA
+constexpr int kRopeWarps = 4;  // per CTA
+constexpr int kRopeStages = 4;     // passes of a warp in shared memory or on their way
+constexpr int kRopeCtasPerSm = 5;  // of the persistent kernel
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -66,8 +78,306 @@ __device__ __forceinline__ float lanes_sum(float x, int L) {
     return x;
 }
 
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+
+// A 16-byte vector as pairs of floats (E elements, E / 2 pairs) and back.
+template <typename T>
+struct Wide;
+template <>
+struct Wide<float> {
+    static constexpr int E = 4;
+    static __device__ __forceinline__ void get(uint4 v, float2 (&x)[2]) {
+        x[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+        x[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    static __device__ __forceinline__ uint4 put(const float2 (&x)[2]) {
+        return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y),
+                          __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+    }
+};
+template <>
+struct Wide<__nv_bfloat16> {
+    static constexpr int E = 8;
+    static __device__ __forceinline__ float2 two(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ void get(uint4 v, float2 (&x)[4]) {
+        x[0] = two(v.x), x[1] = two(v.y), x[2] = two(v.z), x[3] = two(v.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float2 (&x)[4]) {
+        return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
+                          pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
+    }
+};
+template <>
+struct Wide<__half> {
+    static constexpr int E = 8;
+    static __device__ __forceinline__ float2 two(uint32_t w) {
+        return __half22float2(*reinterpret_cast<__half2 *>(&w));
+    }
+    static __device__ __forceinline__ uint32_t pack(float2 x) {
+        const __half2 h = __floats2half2_rn(x.x, x.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ void get(uint4 v, float2 (&x)[4]) {
+        x[0] = two(v.x), x[1] = two(v.y), x[2] = two(v.z), x[3] = two(v.w);
+    }
+    static __device__ __forceinline__ uint4 put(const float2 (&x)[4]) {
+        return make_uint4(pack(x[0]), pack(x[1]), pack(x[2]), pack(x[3]));
+    }
+};
+
+template <typename T, bool INTER, bool NORM>
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_wide_kernel(const RopeArgs A) {
+    using W = Wide<T>;
+    constexpr int E = W::E;  // elements per vector: a lane holds 2 E, E pairs
+    extern __shared__ __align__(128) float rope_smem[];
+    const int pairs = A.rotary / 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // shared memory: the ring [stage][vector][thread] of 16 bytes, each warp's
+    // cosines and sines, the gains of both roles in fp32
+    float *cos_s = rope_smem + kRopeStages * 2 * 32 * kRopeWarps * 4 + warp * 2 * pairs;
+    float *sin_s = cos_s + pairs;
+    float *gain_s = rope_smem + kRopeStages * 2 * 32 * kRopeWarps * 4 + kRopeWarps * 2 * pairs;
+    const uint32_t ring = smem_u32(rope_smem) + threadIdx.x * 16;
+    constexpr uint32_t kVec = 32 * kRopeWarps * 16, kStage = 2 * kVec;
+
+    const int L = A.lanes, HP = 32 / L;
+    const int group = lane / L, sl = lane & (L - 1);
+    // This lane's slot: the element offsets of its two vectors. Slots below
+    // srot turn; the others hold two neighbouring vectors of the part that
+    // passes (the last of them may have one).
+    const int srot = A.rotary / (2 * E);
+    const bool rot = sl < srot;
+    const int o1 = rot && !INTER ? sl * E : (rot ? 2 * sl * E : A.rotary + 2 * (sl - srot) * E);
+    const int o2 = rot && !INTER ? pairs + sl * E : o1 + E;
+    const bool has1 = o1 < A.d, has2 = o2 < A.d;
+
+    const int pq = (A.heads[0] + HP - 1) / HP, passes = pq + (A.heads[1] + HP - 1) / HP;
+    const uint32_t items = static_cast<uint32_t>(A.units) * static_cast<uint32_t>(A.wpt);
+    const uint32_t warps = gridDim.x * kRopeWarps;
+    const uint32_t item0 = blockIdx.x * kRopeWarps + warp;
+
+    // a walk over this warp's passes: queries' passes, then the keys', of each item
+    struct Walk {
+        uint32_t item, unit, b, t;
+        int pass;
+    };
+    const auto enter = [&](Walk &c) {
+        c.unit = A.wpt == 1 ? c.item : c.item / A.wpt;
+        c.pass = static_cast<int>(c.item - c.unit * A.wpt);
+        c.b = A.units == A.tokens ? 0 : c.unit / static_cast<uint32_t>(A.tokens);
+        c.t = c.unit - c.b * static_cast<uint32_t>(A.tokens);
+    };
+    const auto next = [&](Walk &c) {
+        c.pass += A.wpt;
+        if (c.pass >= passes) {
+            c.item += warps;
+            if (c.item < items) enter(c);
+        }
+    };
+    const auto place = [&](const RopeView &v, const Walk &c, int h) {
+        return static_cast<int64_t>(c.b) * v.batch_stride + static_cast<int64_t>(c.t) * v.token_stride +
+               static_cast<int64_t>(h) * v.head_stride;
+    };
+
+    griddep_wait();
+    if constexpr (NORM) {
+        for (int i = threadIdx.x; i < 2 * A.d; i += 32 * kRopeWarps) {
+            const int role = i >= A.d ? 1 : 0, e = i - role * A.d;
+            const void *g = A.gain[role];
+            // channels past d would be read by lanes without a second vector
+            gain_s[role * (A.d + E) + e] =
+                g == nullptr ? 1.f
+                             : (A.gain_f32 ? static_cast<const float *>(g)[e]
+                                           : to_f32(static_cast<const T *>(g)[e]));
+        }
+        if (threadIdx.x < 2 * E)
+            gain_s[(threadIdx.x >= E ? A.d + E : 0) + A.d + threadIdx.x % E] = 0.f;
+        __syncthreads();
+    }
+    if (item0 >= items) return;
+
+    Walk in, out;
+    in.item = out.item = item0;
+    enter(in);
+    enter(out);
+    const auto ask = [&](int stage) {  // the next pass's vectors into the ring
+        if (in.item < items) {
+            const int role = in.pass >= pq ? 1 : 0;
+            const int h = (in.pass - (role ? pq : 0)) * HP + group;
+            if (h < A.heads[role] && has1) {
+                const RopeView &v = A.src[role];
+                const T *src = static_cast<const T *>(v.data) + place(v, in, h);
+                cp_async16(ring + stage * kStage, src + o1);
+                if (has2) cp_async16(ring + stage * kStage + kVec, src + o2);
+            }
+            next(in);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kRopeStages - 1; ++s) ask(s);
+
+    const auto turn = [&](float2 v1, float2 v2, float2 c, float2 s, float2 &y1, float2 &y2) {
+        y1 = ffma2(v2, make_float2(-s.x, -s.y), fmul2(v1, c));
+        y2 = ffma2(v1, s, fmul2(v2, c));
+    };
+    float2 c[E / 2], s[E / 2];
+    const float inv_d = 1.f / static_cast<float>(A.d);
+    uint32_t turned = ~0u;  // the token whose angles c and s hold
+    int stage = 0;
+    while (out.item < items) {
+        if (pairs > 0 && out.unit != turned) {
+            turned = out.unit;
+            const int32_t *pos = A.positions + (out.b * A.pos_batch + out.t) * A.axes;
+            __syncwarp();
+            for (int p = lane; p < pairs; p += 32) {
+                const int64_t at = pos[p < A.axis_pairs ? 0 : 1];
+                const uint64_t angle = static_cast<uint64_t>(at) * A.phases[p];
+                float sn, cs;
+                sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &sn, &cs);
+                cos_s[p] = cs * A.magnitude;
+                sin_s[p] = sn * (A.inverse ? -A.magnitude : A.magnitude);
+            }
+            __syncwarp();
+            if (rot) {
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    c[i] = *reinterpret_cast<const float2 *>(cos_s + sl * E + 2 * i);
+                    s[i] = *reinterpret_cast<const float2 *>(sin_s + sl * E + 2 * i);
+                }
+            }
+        }
+        const int role = out.pass >= pq ? 1 : 0;
+        const int h = (out.pass - (role ? pq : 0)) * HP + group;
+        const bool live = h < A.heads[role] && has1;
+        float2 x[E / 2], y[E / 2];
+        cp_async_wait<kRopeStages - 2>();
+        {
+            uint4 a = make_uint4(0, 0, 0, 0), b = a;
+            if (live) a = ld_shared_v4(ring + stage * kStage);
+            if (live && has2) b = ld_shared_v4(ring + stage * kStage + kVec);
+            W::get(a, x);
+            W::get(b, y);
+        }
+        if constexpr (NORM) {
+            if (A.layer) {
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) sum = fadd2(sum, fadd2(x[i], y[i]));
+                const float mean = lanes_sum(sum.x + sum.y, L) * inv_d;
+                const float2 m1 = has1 ? make_float2(-mean, -mean) : make_float2(0.f, 0.f);
+                const float2 m2 = has2 ? m1 : make_float2(0.f, 0.f);  // no channel, no mean
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    x[i] = fadd2(x[i], m1);
+                    y[i] = fadd2(y[i], m2);
+                }
+            }
+            float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) sq = ffma2(x[i], x[i], ffma2(y[i], y[i], sq));
+            const float rs = rsqrtf(lanes_sum(sq.x + sq.y, L) * inv_d + A.eps);
+            const float2 rr = make_float2(rs, rs);
+            const float *g = gain_s + role * (A.d + E);
+            if (has1) {
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    x[i] = fmul2(x[i], fmul2(rr, *reinterpret_cast<const float2 *>(g + o1 + 2 * i)));
+                    y[i] = fmul2(y[i], fmul2(rr, *reinterpret_cast<const float2 *>(g + o2 + 2 * i)));
+                }
+            }
+        }
+        if (rot) {
+            if constexpr (INTER) {
+                // pairs are neighbours: gather (x1, x1'), (x2, x2') and spread again
+#pragma unroll
+                for (int i = 0; i < E / 4; ++i) {
+                    float2 u, v;
+                    turn(make_float2(x[2 * i].x, x[2 * i + 1].x),
+                         make_float2(x[2 * i].y, x[2 * i + 1].y), c[i], s[i], u, v);
+                    x[2 * i] = make_float2(u.x, v.x), x[2 * i + 1] = make_float2(u.y, v.y);
+                    turn(make_float2(y[2 * i].x, y[2 * i + 1].x),
+                         make_float2(y[2 * i].y, y[2 * i + 1].y), c[E / 4 + i], s[E / 4 + i], u, v);
+                    y[2 * i] = make_float2(u.x, v.x), y[2 * i + 1] = make_float2(u.y, v.y);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    float2 u, v;
+                    turn(x[i], y[i], c[i], s[i], u, v);
+                    x[i] = u, y[i] = v;
+                }
+            }
+        }
+        if (live) {
+            const RopeView &v = A.dst[role];
+            T *dst = static_cast<T *>(v.data) + place(v, out, h);
+            *reinterpret_cast<uint4 *>(dst + o1) = W::put(x);
+            if (has2) *reinterpret_cast<uint4 *>(dst + o2) = W::put(y);
+        }
+        // the slot that this pass's predecessor was read from is free
+        ask(stage == 0 ? kRopeStages - 1 : stage - 1);
+        stage = stage + 1 == kRopeStages ? 0 : stage + 1;
+        next(out);
+    }
+}
+
+template <typename T>
+cudaError_t rope_launch_wide(RopeArgs A, cudaStream_t stream) {
+    constexpr int E = Wide<T>::E;
+    const int slots = A.rotary / (2 * E) + (A.d - A.rotary + 2 * E - 1) / (2 * E);
+    A.lanes = 1;
+    while (A.lanes < slots) A.lanes *= 2;
+    const int HP = 32 / A.lanes;
+    const int64_t passes = (A.heads[0] + HP - 1) / HP + (A.heads[1] + HP - 1) / HP;
+    const int64_t warps = static_cast<int64_t>(kRopeCtasPerSm) * kRopeWarps * sm_count();
+    // warps per token: one, unless that leaves fewer than two items per warp
+    const int64_t want = (2 * warps + A.units - 1) / A.units;
+    A.wpt = static_cast<int>(want < passes ? want : passes);
+    const int64_t ctas = (A.units * A.wpt + kRopeWarps - 1) / kRopeWarps;
+    const int64_t most = static_cast<int64_t>(kRopeCtasPerSm) * sm_count();
+    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
+    const bool norm = A.norm != 0;
+    const size_t smem = kRopeStages * 2 * 32 * kRopeWarps * 16 +
+                        static_cast<size_t>(kRopeWarps) * A.rotary * sizeof(float) +
+                        (norm ? 2 * (A.d + E) * sizeof(float) : 0);
+    void (*kernel)(const RopeArgs) =
+        A.interleaved ? (norm ? rope_wide_kernel<T, true, true> : rope_wide_kernel<T, true, false>)
+                      : (norm ? rope_wide_kernel<T, false, true> : rope_wide_kernel<T, false, false>);
+    return launch_pdl(kernel, grid, dim3(32 * kRopeWarps), smem, stream, A);
+}
+
 template <typename T, int V, bool INTER, bool NORM>
-__global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeArgs A) {
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_any_kernel(const RopeArgs A) {
     constexpr int K = (sizeof(T) == 2 ? 8 : 4) / V;  // slots (pairs of vectors) per lane
     griddep_wait();
     const int lane = threadIdx.x & 31;
@@ -224,7 +534,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const RopeArgs A)
 }
 
 template <typename T, int V>
-cudaError_t rope_launch_v(RopeArgs A, cudaStream_t stream) {
+cudaError_t rope_launch_any(RopeArgs A, cudaStream_t stream) {
     constexpr int K = (sizeof(T) == 2 ? 8 : 4) / V;
     const int slots = A.rotary / (2 * V) + (A.d - A.rotary + 2 * V - 1) / (2 * V);
     A.lanes = 1;
@@ -240,8 +550,8 @@ cudaError_t rope_launch_v(RopeArgs A, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(ctas));
     const bool norm = A.norm != 0;
     void (*kernel)(const RopeArgs) =
-        A.interleaved ? (norm ? rope_kernel<T, V, true, true> : rope_kernel<T, V, true, false>)
-                      : (norm ? rope_kernel<T, V, false, true> : rope_kernel<T, V, false, false>);
+        A.interleaved ? (norm ? rope_any_kernel<T, V, true, true> : rope_any_kernel<T, V, true, false>)
+                      : (norm ? rope_any_kernel<T, V, false, true> : rope_any_kernel<T, V, false, false>);
     return launch_pdl(kernel, grid, dim3(32 * kRopeWarps), 0, stream, A);
 }
 
@@ -259,11 +569,11 @@ cudaError_t rope_launch(const RopeArgs &A, cudaStream_t stream) {
             bits |= static_cast<int64_t>(reinterpret_cast<uintptr_t>(A.gain[r]) /
                                          (A.gain_f32 ? sizeof(float) : sizeof(T)));
     }
+    if (bits % Wide<T>::E == 0) return rope_launch_wide<T>(A, stream);
     if constexpr (sizeof(T) == 2)
-        if (bits % 8 == 0) return rope_launch_v<T, 8>(A, stream);
-    if (bits % 4 == 0) return rope_launch_v<T, 4>(A, stream);
-    if (bits % 2 == 0) return rope_launch_v<T, 2>(A, stream);
-    return rope_launch_v<T, 1>(A, stream);
+        if (bits % 4 == 0) return rope_launch_any<T, 4>(A, stream);
+    if (bits % 2 == 0) return rope_launch_any<T, 2>(A, stream);
+    return rope_launch_any<T, 1>(A, stream);
 }
 
 }  // namespace
