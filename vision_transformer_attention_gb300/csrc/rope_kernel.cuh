@@ -43,7 +43,8 @@ namespace {
 
 constexpr int kRopeWarps = 4;  // per CTA
 constexpr int kRopeStages = 4;     // passes of a warp in shared memory or on their way
-constexpr int kRopeCtasPerSm = 5;  // of the persistent kernel
+// CTAs per SM of the persistent kernel (its registers allow no more)
+constexpr int rope_ctas_per_sm(bool norm) { return norm ? 5 : 6; }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -155,7 +156,8 @@ struct Wide<__half> {
 };
 
 template <typename T, bool INTER, bool NORM>
-__global__ void __launch_bounds__(32 * kRopeWarps) rope_wide_kernel(const RopeArgs A) {
+__global__ void __launch_bounds__(32 * kRopeWarps, rope_ctas_per_sm(NORM))
+rope_wide_kernel(const RopeArgs A) {
     using W = Wide<T>;
     constexpr int E = W::E;  // elements per vector: a lane holds 2 E, E pairs
     extern __shared__ __align__(128) float rope_smem[];
@@ -185,27 +187,44 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_wide_kernel(const RopeAr
     const uint32_t warps = gridDim.x * kRopeWarps;
     const uint32_t item0 = blockIdx.x * kRopeWarps + warp;
 
-    // a walk over this warp's passes: queries' passes, then the keys', of each item
+    // A walk over this warp's passes (the queries', then the keys', of each
+    // item). Inside a role a pass costs two additions; jump() does the rest.
     struct Walk {
-        uint32_t item, unit, b, t;
-        int pass;
+        uint32_t item, unit;
+        int pass, end;  // end: of the role's passes
+        int h, heads;   // this lane's head, the role's heads
+        T *p;           // its first channel
+        int64_t step;
     };
-    const auto enter = [&](Walk &c) {
-        c.unit = A.wpt == 1 ? c.item : c.item / A.wpt;
-        c.pass = static_cast<int>(c.item - c.unit * A.wpt);
-        c.b = A.units == A.tokens ? 0 : c.unit / static_cast<uint32_t>(A.tokens);
-        c.t = c.unit - c.b * static_cast<uint32_t>(A.tokens);
-    };
-    const auto next = [&](Walk &c) {
-        c.pass += A.wpt;
+    const int hs = A.wpt * HP;
+    const auto jump = [&](Walk &c, const RopeView *views) {
         if (c.pass >= passes) {
             c.item += warps;
-            if (c.item < items) enter(c);
+            if (c.item >= items) return;
+            c.unit = A.wpt == 1 ? c.item : c.item / A.wpt;
+            c.pass = static_cast<int>(c.item - c.unit * A.wpt);
         }
+        const uint32_t tokens = static_cast<uint32_t>(A.tokens);
+        const uint32_t b = A.units == A.tokens ? 0 : c.unit / tokens, t = c.unit - b * tokens;
+        const bool key = c.pass >= pq;
+        const RopeView &v = views[key ? 1 : 0];
+        c.end = key ? passes : pq;
+        c.heads = key ? A.heads[1] : A.heads[0];
+        c.h = (c.pass - (key ? pq : 0)) * HP + group;
+        c.p = static_cast<T *>(v.data) + b * v.batch_stride + t * v.token_stride +
+              c.h * v.head_stride;
+        c.step = hs * v.head_stride;
     };
-    const auto place = [&](const RopeView &v, const Walk &c, int h) {
-        return static_cast<int64_t>(c.b) * v.batch_stride + static_cast<int64_t>(c.t) * v.token_stride +
-               static_cast<int64_t>(h) * v.head_stride;
+    const auto next = [&](Walk &c, const RopeView *views) {
+        c.pass += A.wpt;
+        c.h += hs;
+        c.p += c.step;
+        if (c.pass >= c.end) jump(c, views);
+    };
+    const auto start = [&](Walk &c, const RopeView *views) {
+        c.item = item0 - warps;  // jump() moves on to item0
+        c.pass = passes;
+        jump(c, views);
     };
 
     griddep_wait();
@@ -226,38 +245,39 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_wide_kernel(const RopeAr
     if (item0 >= items) return;
 
     Walk in, out;
-    in.item = out.item = item0;
-    enter(in);
-    enter(out);
+    start(in, A.src);
+    start(out, A.dst);
     const auto ask = [&](int stage) {  // the next pass's vectors into the ring
         if (in.item < items) {
-            const int role = in.pass >= pq ? 1 : 0;
-            const int h = (in.pass - (role ? pq : 0)) * HP + group;
-            if (h < A.heads[role] && has1) {
-                const RopeView &v = A.src[role];
-                const T *src = static_cast<const T *>(v.data) + place(v, in, h);
-                cp_async16(ring + stage * kStage, src + o1);
-                if (has2) cp_async16(ring + stage * kStage + kVec, src + o2);
+            if (in.h < in.heads && has1) {
+                cp_async16(ring + stage * kStage, in.p + o1);
+                if (has2) cp_async16(ring + stage * kStage + kVec, in.p + o2);
             }
-            next(in);
+            next(in, A.src);
         }
         cp_async_commit();
     };
 #pragma unroll
     for (int s = 0; s < kRopeStages - 1; ++s) ask(s);
 
-    const auto turn = [&](float2 v1, float2 v2, float2 c, float2 s, float2 &y1, float2 &y2) {
-        y1 = ffma2(v2, make_float2(-s.x, -s.y), fmul2(v1, c));
+    // (c, s, n = -s) of this lane's pairs, two pairs to a float2
+    const auto turn = [&](float2 v1, float2 v2, float2 c, float2 s, float2 n, float2 &y1,
+                          float2 &y2) {
+        y1 = ffma2(v2, n, fmul2(v1, c));
         y2 = ffma2(v1, s, fmul2(v2, c));
     };
-    float2 c[E / 2], s[E / 2];
+    float2 c[E / 2], s[E / 2], n[E / 2];
+    float2 g1[NORM ? E / 2 : 1], g2[NORM ? E / 2 : 1];
     const float inv_d = 1.f / static_cast<float>(A.d);
-    uint32_t turned = ~0u;  // the token whose angles c and s hold
+    uint32_t turned = ~0u;  // the token whose angles c, s and n hold
+    int gains_of = -1;      // the end of the role whose gains g1 and g2 hold
     int stage = 0;
     while (out.item < items) {
         if (pairs > 0 && out.unit != turned) {
             turned = out.unit;
-            const int32_t *pos = A.positions + (out.b * A.pos_batch + out.t) * A.axes;
+            const uint32_t tokens = static_cast<uint32_t>(A.tokens), b = out.unit / tokens;
+            const int32_t *pos =
+                A.positions + (b * A.pos_batch + (out.unit - b * tokens)) * A.axes;
             __syncwarp();
             for (int p = lane; p < pairs; p += 32) {
                 const int64_t at = pos[p < A.axis_pairs ? 0 : 1];
@@ -273,12 +293,24 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_wide_kernel(const RopeAr
                 for (int i = 0; i < E / 2; ++i) {
                     c[i] = *reinterpret_cast<const float2 *>(cos_s + sl * E + 2 * i);
                     s[i] = *reinterpret_cast<const float2 *>(sin_s + sl * E + 2 * i);
+                    n[i] = make_float2(-s[i].x, -s[i].y);
                 }
             }
         }
-        const int role = out.pass >= pq ? 1 : 0;
-        const int h = (out.pass - (role ? pq : 0)) * HP + group;
-        const bool live = h < A.heads[role] && has1;
+        if constexpr (NORM) {
+            if (out.end != gains_of) {
+                gains_of = out.end;
+                const float *g = gain_s + (out.pass >= pq ? A.d + E : 0);
+                if (has1) {
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) {
+                        g1[i] = *reinterpret_cast<const float2 *>(g + o1 + 2 * i);
+                        g2[i] = *reinterpret_cast<const float2 *>(g + o2 + 2 * i);
+                    }
+                }
+            }
+        }
+        const bool live = out.h < out.heads && has1;
         float2 x[E / 2], y[E / 2];
         cp_async_wait<kRopeStages - 2>();
         {
@@ -307,13 +339,10 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_wide_kernel(const RopeAr
             for (int i = 0; i < E / 2; ++i) sq = ffma2(x[i], x[i], ffma2(y[i], y[i], sq));
             const float rs = rsqrtf(lanes_sum(sq.x + sq.y, L) * inv_d + A.eps);
             const float2 rr = make_float2(rs, rs);
-            const float *g = gain_s + role * (A.d + E);
-            if (has1) {
 #pragma unroll
-                for (int i = 0; i < E / 2; ++i) {
-                    x[i] = fmul2(x[i], fmul2(rr, *reinterpret_cast<const float2 *>(g + o1 + 2 * i)));
-                    y[i] = fmul2(y[i], fmul2(rr, *reinterpret_cast<const float2 *>(g + o2 + 2 * i)));
-                }
+            for (int i = 0; i < E / 2; ++i) {
+                x[i] = fmul2(x[i], fmul2(rr, g1[i]));
+                y[i] = fmul2(y[i], fmul2(rr, g2[i]));
             }
         }
         if (rot) {
@@ -323,31 +352,30 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_wide_kernel(const RopeAr
                 for (int i = 0; i < E / 4; ++i) {
                     float2 u, v;
                     turn(make_float2(x[2 * i].x, x[2 * i + 1].x),
-                         make_float2(x[2 * i].y, x[2 * i + 1].y), c[i], s[i], u, v);
+                         make_float2(x[2 * i].y, x[2 * i + 1].y), c[i], s[i], n[i], u, v);
                     x[2 * i] = make_float2(u.x, v.x), x[2 * i + 1] = make_float2(u.y, v.y);
                     turn(make_float2(y[2 * i].x, y[2 * i + 1].x),
-                         make_float2(y[2 * i].y, y[2 * i + 1].y), c[E / 4 + i], s[E / 4 + i], u, v);
+                         make_float2(y[2 * i].y, y[2 * i + 1].y), c[E / 4 + i], s[E / 4 + i],
+                         n[E / 4 + i], u, v);
                     y[2 * i] = make_float2(u.x, v.x), y[2 * i + 1] = make_float2(u.y, v.y);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i) {
                     float2 u, v;
-                    turn(x[i], y[i], c[i], s[i], u, v);
+                    turn(x[i], y[i], c[i], s[i], n[i], u, v);
                     x[i] = u, y[i] = v;
                 }
             }
         }
         if (live) {
-            const RopeView &v = A.dst[role];
-            T *dst = static_cast<T *>(v.data) + place(v, out, h);
-            *reinterpret_cast<uint4 *>(dst + o1) = W::put(x);
-            if (has2) *reinterpret_cast<uint4 *>(dst + o2) = W::put(y);
+            *reinterpret_cast<uint4 *>(out.p + o1) = W::put(x);
+            if (has2) *reinterpret_cast<uint4 *>(out.p + o2) = W::put(y);
         }
         // the slot that this pass's predecessor was read from is free
         ask(stage == 0 ? kRopeStages - 1 : stage - 1);
         stage = stage + 1 == kRopeStages ? 0 : stage + 1;
-        next(out);
+        next(out, A.dst);
     }
 }
 
@@ -359,14 +387,13 @@ cudaError_t rope_launch_wide(RopeArgs A, cudaStream_t stream) {
     while (A.lanes < slots) A.lanes *= 2;
     const int HP = 32 / A.lanes;
     const int64_t passes = (A.heads[0] + HP - 1) / HP + (A.heads[1] + HP - 1) / HP;
-    const int64_t warps = static_cast<int64_t>(kRopeCtasPerSm) * kRopeWarps * sm_count();
+    const bool norm = A.norm != 0;
+    const int64_t most = static_cast<int64_t>(rope_ctas_per_sm(norm)) * sm_count();
     // warps per token: one, unless that leaves fewer than two items per warp
-    const int64_t want = (2 * warps + A.units - 1) / A.units;
+    const int64_t want = (2 * most * kRopeWarps + A.units - 1) / A.units;
     A.wpt = static_cast<int>(want < passes ? want : passes);
     const int64_t ctas = (A.units * A.wpt + kRopeWarps - 1) / kRopeWarps;
-    const int64_t most = static_cast<int64_t>(kRopeCtasPerSm) * sm_count();
     const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
-    const bool norm = A.norm != 0;
     const size_t smem = kRopeStages * 2 * 32 * kRopeWarps * 16 +
                         static_cast<size_t>(kRopeWarps) * A.rotary * sizeof(float) +
                         (norm ? 2 * (A.d + E) * sizeof(float) : 0);
