@@ -35,6 +35,7 @@
 #ifndef VTA_GB300_RPE_ATTN_H
 #define VTA_GB300_RPE_ATTN_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -418,12 +419,70 @@ int qk_norm_rope_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *q_out
                      int64_t batch, int64_t tokens, int heads_q, int heads_k, int d, int dtype,
                      void *stream);
 
+/* Flag of packed_attn_fwd. */
+enum { RPE_ATTN_CAUSAL = 1 };
+
+/*
+ * packed_attn_fwd -- softmax attention over packed sequences of different
+ * lengths, with grouped heads, forward only: images of several resolutions,
+ * prompts, or single query tokens against a cache of keys.
+ *
+ *   out_i = sum_j softmax_j( scale q_i . k_j ) v_j
+ *
+ * Sequence b's queries are rows cu_q[b] .. cu_q[b + 1] of q; its nk keys are
+ * the rows from cu_k[b] on, k_lens[b] of them (k_lens == NULL: up to
+ * cu_k[b + 1]). Query i of nq sees every key, or with RPE_ATTN_CAUSAL the
+ * keys j <= i + nk - nq (the last query sees the last key). Query head h uses
+ * key/value head h / (heads_q / heads_kv).
+ * q, out : [total_q, heads_q, d] views, k, v: [total_k, heads_kv, d] views
+ *          (batch_stride is not read), of bf16 or fp16; 16-byte aligned
+ *          pointers, strides positive multiples of 8 elements. out overlaps
+ *          no input.
+ * lse    : device fp32 [total_q, heads_q] or NULL: ln sum_j exp(scale q_i . k_j).
+ * cu_q, cu_k: device int32 [batch + 1], not decreasing, within [0, total_q]
+ *          and [0, total_k]; k_lens: device int32 [batch] or NULL, between 0
+ *          and cu_k[b + 1] - cu_k[b]. They are read on the device: a value
+ *          outside is clamped, or if sequences overlap some rows are left
+ *          unwritten, and a status bit is set that rpe_device_status reports
+ *          as RPE_ERR_INVALID_ARG; no access leaves the tensors.
+ * scale  : finite, > 0.
+ * A query without a key, or whose scores are all -infinity, gives zeros and
+ * lse -infinity. Rows of out and lse that belong to no sequence stay as they
+ * were. Scores of unseen keys do not matter, NaN included, nor do k and v
+ * behind a sequence's keys; but a v row of the sequence that is infinite or
+ * NaN reaches every query that sees a key of the same 128-key tile of the
+ * sequence.
+ * Scores, maxima, sums and the output accumulate in fp32; the probabilities
+ * are rounded to the 16-bit type before the value product. Results do not
+ * depend on timing (no atomics).
+ * workspace: device memory, 128-byte aligned, of at least the bytes that
+ *          packed_attn_workspace gives for the same sizes (0: may be NULL),
+ *          in use until the call's work on `stream` is done; calls that may
+ *          overlap need one each. The library allocates none but its status
+ *          word: on a device's first call, which inside a stream capture
+ *          therefore returns RPE_ERR_UNSUPPORTED.
+ * Supported: d <= 128 and a multiple of 8, heads_q / heads_kv a whole number
+ * up to 128, total_q and total_k < 2^30 (zero included); anything else, fp32
+ * included, returns RPE_ERR_UNSUPPORTED.
+ */
+int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, const rpe_view *out,
+                    float *lse, const int32_t *cu_q, const int32_t *cu_k, const int32_t *k_lens,
+                    int batch, int64_t total_q, int64_t total_k, int heads_q, int heads_kv, int d,
+                    float scale, unsigned flags, int dtype, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/* packed_attn_workspace -- the bytes of workspace of a packed_attn_fwd call of
+ * these sizes on the current device, in *bytes (host). Errors as there. */
+int packed_attn_workspace(int64_t total_q, int64_t total_k, int batch, int heads_q, int heads_kv,
+                          int d, int dtype, size_t *bytes);
+
 /*
  * rpe_device_status -- synchronises the current device and returns, through
  * *status, the word the kernels set when a bounded wait ran out (bits 0-4)
- * or an offset table held an id out of range (bit 5); 0 = none. Clears the
+ * or an offset table held an id out of range (bit 5) or packed sequences
+ * overlapped or left their tensor (bit 6); 0 = none. Clears the
  * word when `clear` is non-zero. Returns RPE_ERR_TIMEOUT if a wait ran out,
- * else RPE_ERR_INVALID_ARG if a table was bad, RPE_ERR_CUDA if synchronising
+ * else RPE_ERR_INVALID_ARG if a table or a sequence was bad, RPE_ERR_CUDA if synchronising
  * failed, else RPE_OK.
  */
 int rpe_device_status(unsigned *status, int clear);

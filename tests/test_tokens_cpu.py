@@ -1,4 +1,4 @@
-"""Refusals of the calls on tokens (rope_build_phases, rope_fwd, qk_norm_rope_fwd), made on
+"""Refusals of the calls on tokens (rotary positions, norms, packed attention), made on
 the host before any launch, so no GPU is needed."""
 import ctypes
 
@@ -73,3 +73,43 @@ def test_phase_table_refusals(want, kw):
     a.update(kw)
     m = ctypes.c_float(0)
     assert _lib.lib().rope_build_phases(*a.values(), ctypes.byref(m), None) == want
+
+
+def _attn(**kw):
+    a = dict(q=_view(), k=_view(), v=_view(), out=_view(), lse=None, cu_q=FAKE, cu_k=FAKE,
+             k_lens=None, batch=2, total_q=64, total_k=64, hq=4, hkv=2, d=64, scale=0.125, flags=0,
+             dtype=0, workspace=None, bytes=0, stream=None)
+    a.update(kw)
+    return _lib.lib().packed_attn_fwd(*a.values())
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(q=None)), (INVALID, dict(k=None)), (INVALID, dict(v=_view(0))),
+    (INVALID, dict(out=None)), (INVALID, dict(q=_view(FAKE + 8))), (INVALID, dict(v=_view(t=4))),
+    (INVALID, dict(k=_view(h=12))), (INVALID, dict(k=_view(h=0))), (INVALID, dict(out=_view(t=0))),
+    (INVALID, dict(out=_view(t=-256))), (INVALID, dict(cu_q=None)), (INVALID, dict(cu_k=None)),
+    (INVALID, dict(cu_q=FAKE + 2)), (INVALID, dict(k_lens=FAKE + 1)), (INVALID, dict(lse=FAKE + 2)),
+    (INVALID, dict(batch=-1)), (INVALID, dict(total_q=-1)), (INVALID, dict(total_k=-1)),
+    (INVALID, dict(hq=0)), (INVALID, dict(hkv=0)), (INVALID, dict(hq=5)), (INVALID, dict(d=0)),
+    (INVALID, dict(scale=0.0)), (INVALID, dict(scale=-1.0)), (INVALID, dict(scale=float("nan"))),
+    (INVALID, dict(flags=2)), (INVALID, dict(dtype=3)), (UNSUPPORTED, dict(dtype=1)),
+    (UNSUPPORTED, dict(d=136)), (UNSUPPORTED, dict(d=36)), (UNSUPPORTED, dict(hq=258)),
+    (UNSUPPORTED, dict(total_q=1 << 30)), (UNSUPPORTED, dict(total_k=1 << 30)),
+    (UNSUPPORTED, dict(batch=1 << 24)),
+    # one token against 4096 keys runs in pieces and needs its workspace
+    (INVALID, dict(batch=1, total_q=1, total_k=4096)),
+    (INVALID, dict(batch=1, total_q=1, total_k=4096, workspace=FAKE, bytes=64)),
+    (OK, dict(total_q=0, q=None)), (OK, dict(batch=0))])
+def test_packed_attention_refusals(want, kw):
+    assert _attn(**kw) == want
+
+
+def test_packed_attention_workspace_sizes():
+    size = ctypes.c_size_t(7)
+    call = lambda *a: _lib.lib().packed_attn_workspace(*a, ctypes.byref(size))  # noqa: E731
+    assert call(4096, 4096, 4, 8, 2, 64, 0) == OK and size.value == 0
+    assert call(1, 4096, 1, 8, 2, 64, 0) == OK and size.value > 0
+    assert call(0, 4096, 1, 8, 2, 64, 0) == OK and size.value == 0
+    assert call(1, 4096, 1, 8, 3, 64, 0) == INVALID
+    assert call(1, 4096, 1, 8, 2, 64, 1) == UNSUPPORTED
+    assert _lib.lib().packed_attn_workspace(1, 1, 1, 1, 1, 64, 0, None) == INVALID

@@ -28,6 +28,7 @@ RPE_DTYPE_BF16, RPE_DTYPE_F32, RPE_DTYPE_F16 = 0, 1, 2
 RPE_ROPE_NONE, RPE_ROPE_LINEAR, RPE_ROPE_NTK, RPE_ROPE_BANDS, RPE_ROPE_YARN = 0, 1, 2, 3, 4
 RPE_ROPE_INTERLEAVED, RPE_ROPE_INVERSE, RPE_ROPE_BATCH_POSITIONS = 1, 2, 4
 RPE_NORM_RMS, RPE_NORM_LAYER = 0, 1
+RPE_ATTN_CAUSAL = 1
 
 
 class View(ctypes.Structure):
@@ -54,6 +55,10 @@ SIGNATURES = {
                       _i, _p]),
     "qk_norm_rope_fwd": (_i, [_view, _view, _view, _view, _i, _f, _p, _p, _i, _p, _i, _p, _i, _f,
                               _u, _i64, _i64, _i, _i, _i, _i, _p]),
+    "packed_attn_fwd": (_i, [_view, _view, _view, _view, _p, _p, _p, _p, _i, _i64, _i64, _i, _i,
+                             _i, _f, _u, _i, _p, ctypes.c_size_t, _p]),
+    "packed_attn_workspace": (_i, [_i64, _i64, _i, _i, _i, _i, _i,
+                                   ctypes.POINTER(ctypes.c_size_t)]),
     "rpe_device_status": (_i, [ctypes.POINTER(_u), _i]),
     "rpe_wait_probe": (_i, [_u64, _p]),
     "rpe_status_string": (ctypes.c_char_p, [_i]),

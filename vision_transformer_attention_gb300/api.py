@@ -314,6 +314,71 @@ def qk_norm_rope_fwd(q, k, q_gain, k_gain, positions=None, phases=None, norm=_li
     return q_out, k_out
 
 
+def packed_attn_workspace(total_q, total_k, batch, heads_q, heads_kv, d, dtype=torch.bfloat16):
+    """Bytes of workspace that packed_attn_fwd needs for these sizes on the current device."""
+    size = ctypes.c_size_t(0)
+    check("packed_attn_workspace", _lib.lib().packed_attn_workspace(
+        total_q, total_k, batch, heads_q, heads_kv, d, _TOKEN_DTYPES[dtype], ctypes.byref(size)))
+    return size.value
+
+
+def packed_attn_fwd(q, k, v, cu_q, cu_k=None, k_lens=None, causal=False, scale=None, out=None,
+                    return_lse=False, workspace=None):
+    """Softmax attention over packed sequences: q [total_q, heads_q, d], k and v
+    [total_k, heads_kv, d] (bf16 or fp16, any strides that are multiples of 8 with contiguous
+    channels). Sequence b's queries are rows cu_q[b]..cu_q[b + 1], its keys k_lens[b] rows (None:
+    up to cu_k[b + 1]) from cu_k[b] on (cu_k None: as the queries); int32 tensors on q's device.
+    causal: query i of nq sees keys j <= i + nk - nq. scale: 1 / sqrt(d) if None. Rows of a given
+    out that belong to no sequence stay as they were. workspace: a uint8 tensor of at least
+    packed_attn_workspace bytes (None: one is allocated for the call). Returns out, or
+    (out, lse [total_q, heads_q]) with return_lse."""
+    qv = _view(q, "q")
+    dtype, device, shape = q.dtype, q.device, q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [total_q, heads_q, d]")
+    code = _TOKEN_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError("q must be bfloat16 or float16")
+    total_q, heads_q, d = shape
+    kv = _view(k, "k", dtype, None, device)
+    vv = _view(v, "v", dtype, k.shape, device)
+    total_k, heads_kv, d_k = k.shape[-3:]
+    if k.dim() != 3 or d_k != d:
+        raise ValueError(f"k must be [total_k, heads_kv, {d}], got {tuple(k.shape)}")
+    if cu_k is None:
+        cu_k = cu_q
+    _need(cu_q, "cu_q", torch.int32, device=device)
+    batch = cu_q.numel() - 1
+    if batch < 0:
+        raise ValueError("cu_q must have batch + 1 entries")
+    _need(cu_k, "cu_k", torch.int32, (batch + 1,), device)
+    if k_lens is not None:
+        _need(k_lens, "k_lens", torch.int32, (batch,), device)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+    ov = _view(out, "out", dtype, shape, device)
+    lse = torch.empty(total_q, heads_q, dtype=torch.float32, device=device) if return_lse else None
+    if workspace is None:
+        size = ctypes.c_size_t(0)
+        if q.get_device() == torch.cuda.current_device():
+            rc = _lib.lib().packed_attn_workspace(total_q, total_k, batch, heads_q, heads_kv, d, code,
+                                                  ctypes.byref(size))
+        else:
+            with torch.cuda.device(device):
+                rc = _lib.lib().packed_attn_workspace(total_q, total_k, batch, heads_q, heads_kv, d,
+                                                      code, ctypes.byref(size))
+        check("packed_attn_fwd", rc)
+        if size.value:
+            workspace = torch.empty(size.value, dtype=torch.uint8, device=device)
+    else:
+        _need(workspace, "workspace", torch.uint8, device=device)
+    _call(q, "packed_attn_fwd", qv, kv, vv, ov, _ptr(lse), cu_q.data_ptr(), cu_k.data_ptr(),
+          _ptr(k_lens), batch, total_q, total_k, heads_q, heads_kv, d,
+          d ** -0.5 if scale is None else scale, _lib.RPE_ATTN_CAUSAL if causal else 0, code,
+          _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return (out, lse) if return_lse else out
+
+
 def rpe_device_status(clear=True):
     """Synchronises the device; returns the device status word (0 = none; bits
     0-4 a bounded wait ran out, bit 5 an offset table held an id out of range)."""

@@ -86,6 +86,16 @@ unsigned *device_status_word() {
     return g_status[dev];
 }
 
+bool status_word_ready(cudaStream_t stream) {
+    const int dev = current_device();
+    if (dev >= 0) {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (g_status[dev] != nullptr) return true;
+    }
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(stream, &cs) != cudaSuccess || cs == cudaStreamCaptureStatusNone;
+}
+
 bool stream_split_workspace(cudaStream_t stream, size_t floats_per_item, float **ws,
                             int **counters) {
     const int dev = current_device();

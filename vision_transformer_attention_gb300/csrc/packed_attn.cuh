@@ -1,0 +1,945 @@
+// packed_attn.cuh -- softmax attention over packed sequences of different
+// lengths on sm_103a, causal or not, with grouped heads: the kernel template,
+// instantiated for 16-bit types and head sizes by packed_attn_*.cu.
+//
+//   out_i = sum_j softmax_j(scale q_i . k_j) v_j   over the keys j that
+//   query i of its sequence sees (all nk; causal: j <= i + nk - nq).
+//
+// Tiles. The g query heads that share a key/value head sit side by side in
+// memory, so a tile of 128 rows holds TQ = 128 / g tokens x g heads (one TMA
+// box), and every key tile (128 keys) is read once for all of them. Two such
+// tiles are worked on at a time, each by one softmax warpgroup, one thread per
+// row, while one warp issues the tensor-core products of both in turn, so that
+// one tile's softmax runs under the other's products:
+//   whole items (SPLIT = false): two neighbouring tiles of one sequence and
+//     key/value head, sharing every key tile;
+//   pieces (SPLIT = true; few rows, long keys): one tile against a run of key
+//     tiles, the warpgroups taking every other key tile of it. The unnormalised
+//     outputs go to the caller's workspace in fp32 and packed_combine_kernel
+//     joins them. A CTA's runs are its equal share of all key tiles.
+//
+// Per key tile and tile: S = Q K^T into tensor memory (fp32), the row's 128
+// scores into registers, the running maximum, p = 2^(scale log2e (s - m)) in
+// fp32, summed in fp32 and rounded to the 16-bit type over the scores, where
+// the product P V reads its A operand. p <= 2^8 and is at most half a step off
+// (2^-9 for bf16, 2^-12 for fp16 of itself), the precision that the values
+// have. The reference maximum moves only when a row's maximum passes it by
+// more than 2^8; the row's O is rescaled then. O stays in tensor memory.
+//
+// Tensor memory (512 columns): S of the tiles at 0 and 128 (P over S), O at
+// 256 and 256 + D.
+//
+// Keys past a sequence's end and, in the tile on the diagonal, past a row's
+// last key are masked in registers whatever their scores are; V rows past the
+// end are zeroed in shared memory before the product, so that nothing behind a
+// sequence (NaN included) reaches an output.
+#pragma once
+#include "vta_internal.h"
+#include "sm103_ptx.cuh"
+
+#include <type_traits>
+
+namespace vta {
+namespace {
+
+constexpr int kPaThreads = 384;  // two softmax warpgroups, then loads, products, schedule, spare
+constexpr int kPaRegsControl = 64, kPaRegsSoftmax = 216, kPaRegsLaunch = 168;
+static_assert(128 * kPaRegsControl + 256 * kPaRegsSoftmax <= kPaThreads * kPaRegsLaunch, "register split");
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 10;
+constexpr int kWorkSlots = 3;
+constexpr int kKeys = 128;  // keys per tile
+constexpr float kPaRescaleLog2 = 8.f;
+constexpr int kSlab = 128 * 128;  // 128 rows x 64 16-bit channels
+
+template <int D>
+struct PaGeo {
+    static constexpr int SLABS = D / 64;
+    static constexpr int TILE = SLABS * kSlab;  // one Q, K or V tile
+    static constexpr int STAGES = D == 128 ? 5 : 10;  // K and V tiles in flight
+    static constexpr int SMEM = (2 + STAGES) * TILE;
+};
+
+// One unit of work, as the schedule warp hands it to the others.
+struct PaWork {
+    int q_tok;  // first token of the first tile (of all tokens)
+    int toks;   // tokens from there to the end of the sequence
+    int head;   // key/value head; -1: no more work
+    int k_row, nk;  // the sequence's keys
+    int lim0;   // keys that the first token sees (causal; may be <= 0)
+    int lo;     // first key tile
+    int n0, n1; // key tiles of the two tiles (pieces: n0 in all)
+    int slot;   // pieces: where the unnormalised output goes
+};
+
+struct PaBars {
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[10], kv_empty[10];
+    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t w_full[kWorkSlots], w_empty[kWorkSlots];
+    uint64_t fin;
+};
+
+struct PaSeq {
+    int q0, nq, k0, nk;
+};
+
+// Sequence b's rows, clamped into the tensors; *bad if they were not.
+__device__ __forceinline__ PaSeq pa_seq(const PackedAttnArgs &P, int b, bool *bad) {
+    PaSeq s;
+    const int q0 = P.cu_q[b], q1 = P.cu_q[b + 1], k0 = P.cu_k[b], k1 = P.cu_k[b + 1];
+    s.q0 = min(max(q0, 0), P.total_q);
+    s.nq = min(max(q1, s.q0), P.total_q) - s.q0;
+    s.k0 = min(max(k0, 0), P.total_k);
+    s.nk = min(max(k1, s.k0), P.total_k) - s.k0;
+    *bad = *bad || q0 != s.q0 || q1 != s.q0 + s.nq || k0 != s.k0 || k1 != s.k0 + s.nk;
+    if (P.k_lens != nullptr) {
+        const int n = P.k_lens[b];
+        *bad = *bad || n < 0 || n > s.nk;
+        s.nk = min(max(n, 0), s.nk);
+    }
+    return s;
+}
+
+// Key tiles that the tokens up to `last` of a sequence need (at least one, so
+// that rows without keys are written too).
+__device__ __forceinline__ int pa_tiles(const PackedAttnArgs &P, const PaSeq &s, int last) {
+    const int vis = P.causal ? min(s.nk, last + 1 + s.nk - s.nq) : s.nk;
+    return vis <= kKeys ? 1 : (vis + kKeys - 1) / kKeys;
+}
+
+__device__ __forceinline__ int warp_sum(int v) {
+    return __reduce_add_sync(~0u, v);
+}
+__device__ __forceinline__ long long warp_sum64(long long v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+template <typename V>
+__device__ __forceinline__ V warp_scan(V v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const V u = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pa_pack(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pa_pack<__nv_bfloat16>(float lo, float hi) {
+    return pack_bf16x2(lo, hi);
+}
+template <>
+__device__ __forceinline__ uint32_t pa_pack<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Instruction descriptor: fp32 D, A and B both bf16 or both fp16.
+template <typename T>
+__device__ __forceinline__ uint32_t pa_idesc(int N, bool b_mn_major) {
+    const uint32_t f = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+
+// ------------------------------------------------------------- schedule
+
+// Hands PaWork entries to the other roles through a ring in shared memory.
+struct PaRing {
+    PaWork *slots;
+    uint64_t *full, *empty;
+    const WaitCtl *wc;
+    volatile int *abort;
+    int n = 0;
+    // Called by the whole warp with the same values; false: give up.
+    __device__ __forceinline__ bool put(const PaWork &w, int lane) {
+        const int s = n % kWorkSlots, use = n / kWorkSlots;
+        ++n;
+        if (!__all_sync(~0u, mbar_wait(&empty[s], (use & 1) ^ 1, *wc, kStatusTimeoutSync, abort)))
+            return false;
+        if (lane == 0) {
+            slots[s] = w;
+            mbar_arrive(&full[s]);
+        }
+        __syncwarp();
+        return true;
+    }
+};
+
+// Whole items, the costliest first (by key tiles, in at most 64 levels), dealt
+// to the CTAs round by round, every other round backwards.
+__device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRing ring, int lane,
+                                                  int most_tiles) {
+    const int TT = 2 * P.tile_tokens;
+    int shift = 0;
+    while (((most_tiles - 1) >> shift) >= 64) ++shift;
+    long long base = 0;  // items before this level and chunk
+    int round = 0;
+    const auto target = [&]() {
+        const int c = (round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+        return static_cast<long long>(round) * gridDim.x + c;
+    };
+    long long want = target();
+    // items of s with at most (q + 1) << shift key tiles
+    const auto upto = [&](const PaSeq &s, int q) -> int {
+        if (q < 0) return 0;
+        const int nb = (s.nq + TT - 1) / TT;
+        const long long keys = (static_cast<long long>(q + 1) << shift) * kKeys;
+        if (s.nk <= keys) return nb;
+        if (!P.causal) return 0;
+        const long long t = (keys - (s.nk - s.nq)) / TT;
+        return static_cast<int>(t < 0 ? 0 : t > nb ? nb : t);
+    };
+    bool bad = false;
+    PaSeq s{0, 0, 0, 0};
+    bool alive = true;
+    for (int q = (most_tiles - 1) >> shift; alive && q >= 0; --q) {
+        for (int b0 = 0; alive && b0 < P.batch; b0 += 32) {
+            if (P.batch > 32 || q == (most_tiles - 1) >> shift) {
+                s = PaSeq{0, 0, 0, 0};
+                if (b0 + lane < P.batch) s = pa_seq(P, b0 + lane, &bad);
+            }
+            const int high = upto(s, q), mine = high - upto(s, q - 1);
+            const long long sum = warp_scan(static_cast<long long>(mine) * P.heads_kv, lane);
+            const long long all = __shfl_sync(~0u, sum, 31);
+            while (alive && want < base + all) {
+                const uint32_t after = __ballot_sync(~0u, base + sum > want);
+                const int src = __ffs(after) - 1;
+                const long long first = base + sum - static_cast<long long>(mine) * P.heads_kv;
+                const int r = static_cast<int>(want - __shfl_sync(~0u, first, src));
+                PaSeq q_seq{__shfl_sync(~0u, s.q0, src), __shfl_sync(~0u, s.nq, src),
+                            __shfl_sync(~0u, s.k0, src), __shfl_sync(~0u, s.nk, src)};
+                const int t = __shfl_sync(~0u, high, src) - 1 - r / P.heads_kv;
+                const int tok = t * TT;
+                PaWork w;
+                w.q_tok = q_seq.q0 + tok;
+                w.toks = q_seq.nq - tok;
+                w.head = r % P.heads_kv;
+                w.k_row = q_seq.k0;
+                w.nk = q_seq.nk;
+                w.lim0 = tok + 1 + q_seq.nk - q_seq.nq;
+                w.lo = 0;
+                w.n0 = pa_tiles(P, q_seq, min(q_seq.nq, tok + P.tile_tokens) - 1);
+                w.n1 = w.toks > P.tile_tokens ? pa_tiles(P, q_seq, min(q_seq.nq, tok + TT) - 1) : 0;
+                w.slot = 0;
+                alive = ring.put(w, lane);
+                ++round;
+                want = target();
+            }
+            base += all;
+        }
+    }
+    if (alive) {
+        PaWork w{};
+        w.head = -1;
+        ring.put(w, lane);
+    }
+}
+
+// Units (key tiles of one tile and key/value head) and tiles of a sequence.
+__device__ __forceinline__ void pa_units(const PackedAttnArgs &P, const PaSeq &s, long long *units,
+                                         int *tiles) {
+    long long u = 0;
+    const int nt = (s.nq + P.tile_tokens - 1) / P.tile_tokens;
+    if (!P.causal || nt <= 1)
+        u = static_cast<long long>(nt) * (nt ? pa_tiles(P, s, s.nq - 1) : 0);
+    else
+        for (int t = 0; t < nt; ++t)
+            u += pa_tiles(P, s, min(s.nq, (t + 1) * P.tile_tokens) - 1);
+    *units = u * P.heads_kv;
+    *tiles = nt * P.heads_kv;
+}
+
+// Pieces: this CTA's share [u0, u1) of all units, in (sequence, tile, head,
+// key tile) order. per: sequences per warp of the count before.
+__device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRing ring, int lane,
+                                                   const long long *warp_units,
+                                                   const int *warp_tiles, int per) {
+    long long all = 0;
+    int tiles_all = 0;
+    for (int i = 0; i < kPaThreads / 32; ++i) {
+        all += warp_units[i];
+        tiles_all += warp_tiles[i];
+    }
+    PaWork none{};
+    none.head = -1;
+    int *header = static_cast<int *>(P.workspace);
+    if (blockIdx.x == 0 && lane == 0) {
+        *reinterpret_cast<long long *>(header) = all;
+        header[2] = tiles_all <= P.max_items ? tiles_all : 0;
+    }
+    if (tiles_all > P.max_items) {  // overlapping sequences: the workspace is too small
+        if (lane == 0) atomicOr(P.status, kStatusBadSequence);
+        ring.put(none, lane);
+        return;
+    }
+    // no more CTAs than units, so that an item's pieces lie on neighbouring CTAs
+    const long long ctas = all < gridDim.x ? all : gridDim.x;
+    const long long u0 = blockIdx.x < ctas ? all * blockIdx.x / ctas : 0;
+    const long long u1 = blockIdx.x < ctas ? all * (blockIdx.x + 1) / ctas : 0;
+    // the sequence that holds unit u0
+    long long base = 0;
+    int item = 0, i = 0;
+    while (i < kPaThreads / 32 - 1 && base + warp_units[i] <= u0) {
+        base += warp_units[i];
+        item += warp_tiles[i];
+        ++i;
+    }
+    bool bad = false;
+    int b = i * per;
+    PaSeq s{0, 0, 0, 0};
+    if (u0 < u1) {
+        for (;; b += 32) {
+            long long u = 0;
+            int n = 0;
+            s = PaSeq{0, 0, 0, 0};
+            if (b + lane < P.batch) {
+                s = pa_seq(P, b + lane, &bad);
+                pa_units(P, s, &u, &n);
+            }
+            const long long us = warp_scan(u, lane);
+            const int ns = warp_scan(n, lane);
+            const uint32_t after = __ballot_sync(~0u, base + us > u0);
+            if (after != 0u) {
+                const int src = __ffs(after) - 1;
+                base += __shfl_sync(~0u, us - u, src);
+                item += __shfl_sync(~0u, ns - n, src);
+                b += src;
+                s = PaSeq{__shfl_sync(~0u, s.q0, src), __shfl_sync(~0u, s.nq, src),
+                          __shfl_sync(~0u, s.k0, src), __shfl_sync(~0u, s.nk, src)};
+                break;
+            }
+            base += __shfl_sync(~0u, us, 31);
+            item += __shfl_sync(~0u, ns, 31);
+            if (b >= P.batch) {  // cannot happen: u0 < all
+                ring.put(none, lane);
+                return;
+            }
+        }
+    }
+    long long u = u0;
+    int4 *meta = reinterpret_cast<int4 *>(header + 16);
+    for (int t = 0; u < u1;) {
+        const int last = min(s.nq, (t + 1) * P.tile_tokens) - 1;
+        const int kt = pa_tiles(P, s, last);
+        const long long span = static_cast<long long>(kt) * P.heads_kv;
+        if (t * P.tile_tokens >= s.nq) {  // next sequence
+            ++b;
+            t = 0;
+            if (b >= P.batch) break;
+            s = pa_seq(P, b, &bad);
+            continue;
+        }
+        if (base + span <= u) {
+            base += span;
+            item += P.heads_kv;
+            ++t;
+            continue;
+        }
+        const int h = static_cast<int>((u - base) / kt);
+        const long long first = base + static_cast<long long>(h) * kt;  // the item's first unit
+        const int lo = static_cast<int>(u - first);
+        const int n = static_cast<int>(u1 - u < kt - lo ? u1 - u : kt - lo);
+        const int tok = t * P.tile_tokens;
+        PaWork w;
+        w.q_tok = s.q0 + tok;
+        w.toks = min(s.nq - tok, P.tile_tokens);
+        w.head = h;
+        w.k_row = s.k0;
+        w.nk = s.nk;
+        w.lim0 = tok + 1 + s.nk - s.nq;
+        w.lo = lo;
+        w.n0 = n;
+        w.n1 = 0;
+        w.slot = item + h + blockIdx.x;
+        if (lo == 0 && lane == 0) {
+            meta[2 * (item + h)] = make_int4(static_cast<int>(first & 0xFFFFFFFFll),
+                                             static_cast<int>(first >> 32), kt, w.q_tok);
+            meta[2 * (item + h) + 1] = make_int4(w.toks, h, 0, 0);
+        }
+        if (!ring.put(w, lane)) return;
+        u += n;
+    }
+    ring.put(none, lane);
+}
+
+// ------------------------------------------------------------- the kernel
+
+template <typename T, int D, bool SPLIT>
+__global__ void __launch_bounds__(kPaThreads, 1)
+packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PackedAttnArgs P) {
+    using G = PaGeo<D>;
+    extern __shared__ __align__(1024) uint8_t pa_smem[];
+    __shared__ PaBars bars;
+    __shared__ PaWork work[kWorkSlots];
+    __shared__ long long warp_units[kPaThreads / 32];
+    __shared__ int warp_tiles[kPaThreads / 32];
+    __shared__ uint32_t tmem_base_s;
+    __shared__ volatile int abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const WaitCtl wc{P.status, kDefaultWaitNs};
+    const WaitCtl drain{P.status, kDefaultWaitNs};
+    uint8_t *sQ = pa_smem, *sKV = pa_smem + 2 * G::TILE;
+
+    if (tid == 0) {
+        mbar_init(&bars.q_full, 1);
+        mbar_init(&bars.q_empty, 1);
+        for (int i = 0; i < G::STAGES; ++i) {
+            mbar_init(&bars.kv_full[i], 1);
+            mbar_init(&bars.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.o_full[i], 1);
+            mbar_init(&bars.o_empty[i], 4);
+        }
+        for (int i = 0; i < kWorkSlots; ++i) {
+            mbar_init(&bars.w_full[i], 1);
+            mbar_init(&bars.w_empty[i], 10);
+        }
+        mbar_init(&bars.fin, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(&tmem_base_s, 512);
+    griddep_wait();
+    griddep_launch_dependents();
+    // Count before the roles part: units and tiles (pieces) or the most key
+    // tiles of a sequence (whole items), each warp over its run of sequences.
+    const int per = (P.batch + kPaThreads - 1) / kPaThreads * 32;
+    {
+        bool bad = false;
+        long long units = 0;
+        int tiles = 0;
+        for (int i = 0; i < per; i += 32) {
+            const int b = warp * per + i + lane;
+            if (b >= P.batch) continue;
+            const PaSeq s = pa_seq(P, b, &bad);
+            if constexpr (SPLIT) {
+                long long u;
+                int n;
+                pa_units(P, s, &u, &n);
+                units += u;
+                tiles += n;
+            } else {
+                tiles = max(tiles, pa_tiles(P, s, s.nq - 1));
+            }
+        }
+        if (bad) atomicOr(P.status, kStatusBadSequence);
+        if constexpr (SPLIT) {
+            units = warp_sum64(units);
+            tiles = warp_sum(tiles);
+        } else {
+            tiles = __reduce_max_sync(~0u, tiles);
+        }
+        if (lane == 0) {
+            warp_units[warp] = units;
+            warp_tiles[warp] = tiles;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+
+    // The next entry of the schedule; every role walks the same list.
+    int wn = 0;
+    const auto next_work = [&](PaWork &w) -> bool {  // by the whole warp
+        const int s = wn % kWorkSlots, use = wn / kWorkSlots;
+        ++wn;
+        if (!__all_sync(~0u, mbar_wait(&bars.w_full[s], use & 1, wc, kStatusTimeoutSync, &abort_flag)))
+            return false;
+        w = work[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.w_empty[s]);
+        return w.head >= 0;
+    };
+
+    if (warp >= 8) {
+        regs_dealloc<kPaRegsControl>();
+        if (warp == kWarpSched) {
+            PaRing ring{work, bars.w_full, bars.w_empty, &wc, &abort_flag};
+            if constexpr (SPLIT) {
+                pa_schedule_pieces(P, ring, lane, warp_units, warp_tiles, per);
+            } else {
+                int most = 1;
+                for (int i = 0; i < kPaThreads / 32; ++i) most = max(most, warp_tiles[i]);
+                pa_schedule_items(P, ring, lane, most);
+            }
+        } else if (warp == kWarpLoad) {
+            if (lane == 0) {
+                prefetch_tmap(&tm_q);
+                prefetch_tmap(&tm_k);
+                prefetch_tmap(&tm_v);
+            }
+            int g = 0, it = 0;  // K and V tiles, items
+            bool ok = true;
+            const uint32_t q_bytes = 128u * P.group * P.tile_tokens * G::SLABS;
+            PaWork w;
+            for (; ok && next_work(w); ++it) {
+                ok = __all_sync(~0u, mbar_wait(&bars.q_empty, (it & 1) ^ 1, wc, kStatusTimeoutSync,
+                                               &abort_flag));
+                if (!ok) break;
+                const int tiles_q = SPLIT ? 1 : (w.n1 > 0 ? 2 : 1);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars.q_full, tiles_q * q_bytes);
+                    for (int i = 0; i < tiles_q; ++i)
+                        for (int sl = 0; sl < G::SLABS; ++sl)
+                            tma_load_3d(sQ + i * G::TILE + sl * kSlab, &tm_q, &bars.q_full, sl * 64,
+                                        w.head * P.group, w.q_tok + i * P.tile_tokens);
+                }
+                const int n = max(w.n0, w.n1);
+                // K0, then K(j + 1), V(j): the order in which they are used
+                for (int j = 0; j < 2 * n; ++j, ++g) {
+                    const bool is_k = j == 0 || ((j & 1) != 0 && j < 2 * n - 1);
+                    const int kt = is_k ? (j + 1) / 2 : (j == 2 * n - 1 ? n - 1 : j / 2 - 1);
+                    const int st = g % G::STAGES, use = g / G::STAGES;
+                    ok = __all_sync(~0u, mbar_wait(&bars.kv_empty[st], (use & 1) ^ 1, wc,
+                                                   kStatusTimeoutSync, &abort_flag));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bars.kv_full[st], G::TILE);
+                        for (int sl = 0; sl < G::SLABS; ++sl)
+                            tma_load_3d(sKV + st * G::TILE + sl * kSlab, is_k ? &tm_k : &tm_v,
+                                        &bars.kv_full[st], sl * 64, w.head,
+                                        w.k_row + (w.lo + kt) * kKeys);
+                    }
+                }
+            }
+            // drain: the most recent load on every barrier has landed
+            if (it > 0 && lane == 0) {
+                mbar_wait(&bars.q_full, (it - 1) & 1, drain, kStatusTimeoutDrain, nullptr);
+                for (int st = 0; st < G::STAGES; ++st) {
+                    const int uses = (g - st + G::STAGES - 1) / G::STAGES;  // loads into this stage
+                    if (uses > 0)
+                        mbar_wait(&bars.kv_full[st], (uses - 1) & 1, drain, kStatusTimeoutDrain, nullptr);
+                }
+            }
+            __syncwarp();
+        } else if (warp == kWarpMma) {
+            const uint64_t k_major = smem_desc(0, 16, 1024, kSwizzle128B);
+            const uint64_t mn_major = smem_desc(0, kSlab, 1024, kSwizzle128B);
+            const uint32_t aQ = smem_u32(sQ), aKV = smem_u32(sKV);
+            const int q_steps = (P.d + 15) / 16, d16 = q_steps * 16;
+            const uint32_t id_s = pa_idesc<T>(kKeys, false), id_o = pa_idesc<T>(d16, true);
+            const bool lead = lane == 0;
+            int g = 0, it = 0;
+            int np[2] = {0, 0};   // P tiles consumed, per tile
+            int no[2] = {0, 0};   // items finished, per tile
+            bool ok = true;
+            PaWork w;
+
+            const auto kv_wait = [&](int idx) {
+                const int st = idx % G::STAGES, use = idx / G::STAGES;
+                ok = ok && __all_sync(~0u, mbar_wait(&bars.kv_full[st], use & 1, wc, kStatusTimeoutLoad,
+                                                     &abort_flag, false));
+                return st;
+            };
+            const auto kv_free = [&](int st) {
+                if (lead) mma_commit(&bars.kv_empty[st]);
+            };
+            // S of tile x = Q (tile qx) K^T
+            const auto qk = [&](int x, int qx, int st) {
+                if (lead) {
+                    for (int kk = 0; kk < q_steps; ++kk) {
+                        const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
+                        mma_bf16_ss(tmem + x * 128, k_major | ((aQ + qx * G::TILE + off) >> 4),
+                                    k_major | ((aKV + st * G::TILE + off) >> 4), id_s, kk > 0);
+                    }
+                    mma_commit(&bars.s_full[x]);
+                }
+            };
+            // 16-key steps of key tile kt of the sequence that hold keys (at
+            // least one); V rows of the last one behind the sequence become zero
+            const auto steps_of = [&](int kt, int st) {
+                const int left = w.nk - kt * kKeys;
+                if (left >= kKeys) return kKeys / 16;
+                const int keys = max(left, 0), steps = max((keys + 15) / 16, 1);
+                for (int sl = 0; sl < G::SLABS; ++sl)
+                    for (int i = keys * 8 + lane; i < steps * 128; i += 32)
+                        st_shared_v4(aKV + st * G::TILE + sl * kSlab + i * 16, 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                return steps;
+            };
+            const auto pv = [&](int x, int st, int steps, bool first) {
+                if (!ok) return;
+                ok = __all_sync(~0u, mbar_wait(&bars.p_full[x], np[x] & 1, wc, kStatusTimeoutSync,
+                                               &abort_flag, false));
+                ++np[x];
+                if (first)
+                    ok = ok && __all_sync(~0u, mbar_wait(&bars.o_empty[x], (no[x] & 1) ^ 1, wc,
+                                                         kStatusTimeoutSync, &abort_flag, false));
+                if (!ok) return;
+                tc_fence_after();
+                if (lead)
+                    for (int kk = 0; kk < steps; ++kk)
+                        mma_bf16_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8,
+                                    mn_major | ((aKV + st * G::TILE + kk * 2048) >> 4), id_o,
+                                    kk > 0 || !first);
+            };
+            const auto finish = [&](int x) {
+                if (lead) mma_commit(&bars.o_full[x]);
+                ++no[x];
+            };
+            for (; ok && next_work(w); ++it) {
+                ok = ok && __all_sync(~0u, mbar_wait(&bars.q_full, it & 1, wc, kStatusTimeoutLoad,
+                                                     &abort_flag, false));
+                if (!ok) break;
+                tc_fence_after();
+                const int n = max(w.n0, w.n1);
+                int st = kv_wait(g);
+                if (!ok) break;
+                if constexpr (!SPLIT) {
+                    if (w.n0 > 0) qk(0, 0, st);
+                    if (w.n1 > 0) qk(1, 1, st);
+                    kv_free(st);
+                    for (int j = 0; ok && j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        const int sk = more ? kv_wait(g + 2 * j + 1) : 0;
+                        const int sv = kv_wait(g + 2 * j + (more ? 2 : 1));
+                        if (!ok) break;
+                        const int steps = steps_of(j, sv);
+                        for (int x = 0; x < 2; ++x) {
+                            const int nx = x ? w.n1 : w.n0;
+                            if (j >= nx) continue;
+                            pv(x, sv, steps, j == 0);
+                            if (!ok) break;
+                            if (j + 1 < nx)
+                                qk(x, x, sk);
+                            else
+                                finish(x);
+                        }
+                        if (!ok) break;
+                        if (more) kv_free(sk);
+                        kv_free(sv);
+                        if (j == n - 2 || n == 1)
+                            if (lead) mma_commit(&bars.q_empty);
+                    }
+                } else {
+                    qk(0, 0, st);
+                    kv_free(st);
+                    for (int j = 0; ok && j < n; ++j) {
+                        const int x = j & 1;
+                        if (j + 1 < n) {
+                            const int sk = kv_wait(g + 2 * j + 1);
+                            if (!ok) break;
+                            // tile x ^ 1's scores are free once its last P V is issued
+                            qk(x ^ 1, 0, sk);
+                            kv_free(sk);
+                        }
+                        if (j + 2 >= n && (j + 1 < n || n == 1))
+                            if (lead) mma_commit(&bars.q_empty);
+                        const int sv = kv_wait(g + 2 * j + (j + 1 < n ? 2 : 1));
+                        if (!ok) break;
+                        const int steps = steps_of(w.lo + j, sv);
+                        pv(x, sv, steps, j < 2);
+                        if (!ok) break;
+                        kv_free(sv);
+                        if (j + 2 >= n) finish(x);
+                    }
+                }
+                g += 2 * n;
+            }
+            // drain: a last commit completes after every product issued here
+            if (lead) {
+                mma_commit(&bars.fin);
+                mbar_wait(&bars.fin, 0, drain, kStatusTimeoutDrain, nullptr);
+            }
+            __syncwarp();
+        }
+    } else {
+        regs_alloc<kPaRegsSoftmax>();
+        const int x = warp >> 2;                     // which tile
+        const int row = tid & 127;                   // of the tile
+        const int tok = row / P.group, hd = row - tok * P.group;
+        const int tok_first = (row & ~31) / P.group; // token of the warp's first row
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field: 32 * warp
+        const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * D;
+        int ns = 0, no = 0;
+        const float c = P.scale_log2;
+        const float2 c2 = make_float2(c, c);
+        PaWork w;
+        bool ok = true;
+        while (ok && next_work(w)) {
+            const int n = SPLIT ? (w.n0 + 1 - x) / 2 : (x ? w.n1 : w.n0);
+            const int shift_tok = SPLIT ? 0 : x * P.tile_tokens;
+            const int toks = min(w.toks - shift_tok, P.tile_tokens);  // of this tile
+            const bool valid = tok < toks;
+            int lim = P.causal ? min(w.nk, w.lim0 + shift_tok + tok) : w.nk;
+            // masking is tested per warp against its first row, which sees least
+            const int lim_first = P.causal ? min(w.nk, w.lim0 + shift_tok + tok_first) : w.nk;
+            const bool warp_live = tok_first < toks && tok_first < P.tile_tokens;
+            float m = -INFINITY, l = 0.f;
+            for (int i = 0; i < n; ++i, ++ns) {
+                const int kt = SPLIT ? w.lo + 2 * i + x : i;
+                ok = __all_sync(~0u, mbar_wait(&bars.s_full[x], ns & 1, wc, kStatusTimeoutMma, &abort_flag,
+                                               false));
+                if (!ok) break;
+                if (warp_live) {
+                    tc_fence_after();
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, s[q]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ready(s[q]);
+                    const int seen = lim - kt * kKeys;  // columns that this row sees
+                    if (lim_first < (kt + 1) * kKeys) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (q * 32 + e >= seen) s[q][e] = 0xFF800000u;  // -inf
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float t[11];
+#pragma unroll
+                        for (int e = 0; e < 10; ++e)
+                            t[e] = fmax3(__uint_as_float(s[q][3 * e]), __uint_as_float(s[q][3 * e + 1]),
+                                         __uint_as_float(s[q][3 * e + 2]));
+                        t[10] = fmaxf(__uint_as_float(s[q][30]), __uint_as_float(s[q][31]));
+                        const float a = fmax3(t[0], t[1], t[2]), b = fmax3(t[3], t[4], t[5]);
+                        const float d = fmax3(t[6], t[7], t[8]);
+                        mx = fmax3(mx, fmax3(a, b, d), fmaxf(t[9], t[10]));
+                    }
+                    mx *= c;
+                    const bool grow = mx > m + kPaRescaleLog2 || (m == -INFINITY && mx > m);
+                    if (__any_sync(~0u, grow)) {
+                        const float alpha = grow ? (m == -INFINITY ? 0.f : ex2_approx(m - mx)) : 1.f;
+                        if (grow) m = mx;
+                        l *= alpha;
+                        if (i > 0) {
+                            // every earlier product of this tile is complete: the commit
+                            // behind these scores covers it
+#pragma unroll 1
+                            for (int r = 0; r < D / 16; ++r) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + r * 16, o);
+                                tmem_ld_wait(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(tO + r * 16, o);
+                            }
+                        }
+                    }
+                    const float mm = m == -INFINITY ? 0.f : m;
+                    const float2 nm = make_float2(-mm, -mm);
+                    float2 sum[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
+                        sum[q] = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = ffma2(make_float2(__uint_as_float(s[q][2 * e]),
+                                                               __uint_as_float(s[q][2 * e + 1])),
+                                                   c2, nm);
+                            const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                            sum[q] = fadd2(sum[q], p);
+                            pk[e] = pa_pack<T>(p.x, p.y);
+                        }
+                        tmem_st16(tS + q * 16, pk);
+                    }
+                    const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                    l += t.x + t.y;
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[x]);
+            }
+            if (!ok) break;
+            if (n > 0) {
+                ok = __all_sync(~0u, mbar_wait(&bars.o_full[x], no & 1, wc, kStatusTimeoutMma, &abort_flag,
+                                               false));
+                if (!ok) break;
+                ++no;
+                tc_fence_after();
+            }
+            if constexpr (SPLIT) {
+                const int64_t at = (static_cast<int64_t>(w.slot) * 2 + x) * P.ws_rows + row;
+                const bool mine = valid && row < P.ws_rows;
+                if (mine) P.ws_ml[at] = make_float2(n > 0 ? m : -INFINITY, n > 0 ? l : 0.f);
+                if (warp_live && n > 0) {
+                    float *dst = P.ws_o + at * D;
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + q * 32, o);
+                        tmem_ld_wait(o);
+                        if (mine)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4 *>(dst + q * 32 + e) =
+                                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+            } else if (warp_live && n > 0) {
+                // a row that sees no key (or only scores of -inf) gives zeros
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int64_t token = w.q_tok + shift_tok + tok;
+                const int64_t head = static_cast<int64_t>(w.head) * P.group + hd;
+                T *dst = static_cast<T *>(P.out) + token * P.out_token + head * P.out_head;
+                if (valid && P.lse != nullptr)
+                    P.lse[token * P.group * P.heads_kv + head] =
+                        l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + q * 32, o);
+                    tmem_ld_wait(o);
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            if (q * 32 + e < P.d) {
+                                uint32_t v[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float a = __uint_as_float(o[e + 2 * k]) * inv;
+                                    const float b = __uint_as_float(o[e + 2 * k + 1]) * inv;
+                                    v[k] = l == 0.f ? 0u : pa_pack<T>(a, b);
+                                }
+                                *reinterpret_cast<uint4 *>(dst + q * 32 + e) =
+                                    make_uint4(v[0], v[1], v[2], v[3]);
+                            }
+                    }
+                }
+            }
+            if (n > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.o_empty[x]);
+            }
+        }
+    }
+    tc_fence_before();
+    asm volatile("barrier.sync 0;" ::: "memory");
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the pieces of the tiles: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p.
+// WIDE: a CTA per row, its warps taking every eighth piece (few rows, many
+// pieces); otherwise a warp per row.
+constexpr int kJoinWarps = 8;
+
+template <typename T, int D, bool WIDE>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int grid) {
+    constexpr int C = D / 32;  // columns per lane
+    __shared__ float part[WIDE ? kJoinWarps : 1][WIDE ? D : 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blocks = WIDE ? P.ws_rows : (P.ws_rows + kJoinWarps - 1) / kJoinWarps;
+    const int item = blockIdx.x / blocks;
+    const int row = WIDE ? blockIdx.x - item * blocks : (blockIdx.x - item * blocks) * kJoinWarps + warp;
+    griddep_wait();
+    const int *header = static_cast<const int *>(P.workspace);
+    const long long all = *reinterpret_cast<const long long *>(header);
+    if (item >= header[2] || row >= P.ws_rows) return;
+    const int4 *meta = reinterpret_cast<const int4 *>(header + 16) + 2 * item;
+    const int4 a = meta[0], b = meta[1];
+    const int tok = row / P.group;
+    if (tok >= b.x) return;
+    const long long first = (static_cast<long long>(a.y) << 32) | static_cast<uint32_t>(a.x);
+    const long long ctas = all < grid ? all : grid;
+    const int c0 = static_cast<int>(((first + 1) * ctas - 1) / all);
+    const int c1 = static_cast<int>(((first + a.z) * ctas - 1) / all);
+    const int pieces = 2 * (c1 - c0 + 1);
+    const auto at = [&](int p) {
+        return (static_cast<int64_t>(item + c0) * 2 + p) * P.ws_rows + row;
+    };
+    float M = -INFINITY;
+    for (int p = lane; p < pieces; p += 32) M = fmaxf(M, P.ws_ml[at(p)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int p = lane; p < pieces; p += 32) {
+        const float2 ml = P.ws_ml[at(p)];
+        if (ml.y != 0.f) L += ml.y * ex2_approx(ml.x - base);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
+    float acc[C];
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int p = WIDE ? warp : 0; p < pieces; p += WIDE ? kJoinWarps : 1) {
+        const int64_t i = at(p);
+        const float2 ml = P.ws_ml[i];
+        if (ml.y == 0.f) continue;  // no key seen: nothing was written
+        const float f = ex2_approx(ml.x - base);
+        const float *src = P.ws_o + i * D + lane * C;
+        if constexpr (C == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src);
+            acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(src);
+            acc[0] += f * v.x, acc[1] += f * v.y;
+        }
+    }
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int e = 0; e < C; ++e) part[warp][lane * C + e] = acc[e];
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < kJoinWarps; ++i) s += part[i][lane * C + e];
+            acc[e] = s;
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t token = a.w + tok;
+    const int64_t head = static_cast<int64_t>(b.y) * P.group + (row - tok * P.group);
+    if (lane == 0 && P.lse != nullptr)
+        P.lse[token * P.group * P.heads_kv + head] =
+            L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+    if (lane * C >= P.d) return;
+    T *dst = static_cast<T *>(P.out) + token * P.out_token + head * P.out_head + lane * C;
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc[e] = L == 0.f ? 0.f : acc[e] * inv;
+    if constexpr (C == 4)
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(pa_pack<T>(acc[0], acc[1]), pa_pack<T>(acc[2], acc[3]));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pa_pack<T>(acc[0], acc[1]);
+}
+
+template <typename T, int D>
+cudaError_t pa_launch(const PackedAttnMaps &m, const PackedAttnArgs &a, bool pieces, int ctas,
+                      cudaStream_t stream) {
+    void (*kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PackedAttnArgs) =
+        pieces ? packed_attn_kernel<T, D, true> : packed_attn_kernel<T, D, false>;
+    cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           PaGeo<D>::SMEM);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(kernel, dim3(ctas), dim3(kPaThreads), PaGeo<D>::SMEM, stream, m.q, m.k, m.v, a);
+    if (err != cudaSuccess || !pieces) return err;
+    const int64_t rows = static_cast<int64_t>(a.max_items) * a.ws_rows;
+    if (rows <= 16 * sm_count())
+        return launch_pdl(packed_combine_kernel<T, D, true>, dim3(static_cast<unsigned>(rows)),
+                          dim3(32 * kJoinWarps), 0, stream, a, ctas);
+    const int blocks = (a.ws_rows + kJoinWarps - 1) / kJoinWarps;
+    return launch_pdl(packed_combine_kernel<T, D, false>,
+                      dim3(static_cast<unsigned>(a.max_items) * blocks), dim3(32 * kJoinWarps), 0,
+                      stream, a, ctas);
+}
+
+}  // namespace
+}  // namespace vta

@@ -21,6 +21,7 @@ enum : unsigned {
     kStatusTimeoutDrain = 1u << 3,  // draining in-flight work after an abort ran out
     kStatusTimeoutProbe = 1u << 4,  // the self-test wait (nothing ever arrives)
     kStatusBadBucket = 1u << 5,     // an offset table held an id outside [0, bound)
+    kStatusBadSequence = 1u << 6,   // packed sequences overlapped or left their tensor
 };
 constexpr unsigned kStatusTimeoutMask = 0x1Fu;
 

@@ -15,6 +15,9 @@ struct WaitCtl;
 // Device status word of the current device (allocated on first use; NULL if
 // that failed) and the default bound on in-kernel waits.
 unsigned *device_status_word();
+// False while the word does not exist yet and `stream` is being captured (the
+// allocation would break the capture).
+bool status_word_ready(cudaStream_t stream);
 
 // Workspace of the split tail items of the two-warpgroup kernel for launches on
 // `stream` of the current device: floats_per_item fp32 for each of up to
@@ -162,6 +165,34 @@ struct RopeArgs {
 cudaError_t launch_rope_bf16(const RopeArgs &a, cudaStream_t stream);
 cudaError_t launch_rope_f16(const RopeArgs &a, cudaStream_t stream);
 cudaError_t launch_rope_f32(const RopeArgs &a, cudaStream_t stream);
+
+// Attention over packed sequences (packed_attn.cuh).
+struct PackedAttnArgs {
+    const int32_t *cu_q, *cu_k, *k_lens;  // [batch + 1], [batch + 1], [batch] or NULL
+    int batch, total_q, total_k, heads_kv, group, d;
+    int tile_tokens;  // tokens of a 128-row tile: 128 / group
+    int causal;
+    float scale_log2;  // scale * log2(e)
+    void *out;
+    int64_t out_token, out_head;
+    float *lse;  // [total_q, heads_q] or NULL
+    // pieces: the workspace (a header, two int4 per item), the row maxima and
+    // sums, the unnormalised outputs [slot][2][ws_rows][D]
+    void *workspace;
+    float2 *ws_ml;
+    float *ws_o;
+    int ws_rows, max_items;
+    unsigned *status;
+};
+struct PackedAttnMaps {
+    CUtensorMap q, k, v;
+};
+// pieces: the kernel that writes unnormalised pieces on `ctas` CTAs, then the
+// one that joins them; otherwise whole items on `ctas` CTAs. bf16: the type.
+cudaError_t launch_packed_attn_d64(const PackedAttnMaps &m, const PackedAttnArgs &a, bool bf16,
+                                   bool pieces, int ctas, cudaStream_t stream);
+cudaError_t launch_packed_attn_d128(const PackedAttnMaps &m, const PackedAttnArgs &a, bool bf16,
+                                    bool pieces, int ctas, cudaStream_t stream);
 
 cudaError_t launch_wait_probe(unsigned long long limit_ns, cudaStream_t stream);
 
