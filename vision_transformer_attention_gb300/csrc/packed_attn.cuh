@@ -42,8 +42,8 @@
 namespace vta {
 namespace {
 
-constexpr int kPaThreads = 384;  // two softmax warpgroups, then loads, products, schedule, spare
-constexpr int kPaRegsControl = 64, kPaRegsSoftmax = 216, kPaRegsLaunch = 168;
+constexpr int kPaThreads = 384;  // two softmax warpgroups, then loads, products, schedule, V tails
+constexpr int kPaRegsControl = 80, kPaRegsSoftmax = 208, kPaRegsLaunch = 168;
 static_assert(128 * kPaRegsControl + 256 * kPaRegsSoftmax <= kPaThreads * kPaRegsLaunch, "register split");
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 10;
 constexpr int kWorkSlots = 3;
@@ -76,7 +76,7 @@ struct PaBars {
     uint64_t kv_full[10], kv_empty[10];
     uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
     uint64_t w_full[kWorkSlots], w_empty[kWorkSlots];
-    uint64_t fin;
+    uint64_t v_ask, v_fixed, fin;
 };
 
 struct PaSeq {
@@ -401,8 +401,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int i = 0; i < kWorkSlots; ++i) {
             mbar_init(&bars.w_full[i], 1);
-            mbar_init(&bars.w_empty[i], 10);
+            mbar_init(&bars.w_empty[i], 11);
         }
+        mbar_init(&bars.v_ask, 1);
+        mbar_init(&bars.v_fixed, 1);
         mbar_init(&bars.fin, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -448,15 +450,20 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
 
-    // The next entry of the schedule; every role walks the same list.
+    // The next entry of the schedule; every role walks the same list (a whole
+    // warp, or for the products its first lane).
     int wn = 0;
-    const auto next_work = [&](PaWork &w) -> bool {  // by the whole warp
+    const auto next_work = [&](PaWork &w) -> bool {
         const int s = wn % kWorkSlots, use = wn / kWorkSlots;
         ++wn;
-        if (!__all_sync(~0u, mbar_wait(&bars.w_full[s], use & 1, wc, kStatusTimeoutSync, &abort_flag)))
+        const bool ok = mbar_wait(&bars.w_full[s], use & 1, wc, kStatusTimeoutSync, &abort_flag);
+        if (warp == kWarpMma) {
+            if (!ok) return false;
+        } else if (!__all_sync(~0u, ok)) {
             return false;
+        }
         w = work[s];
-        __syncwarp();
+        if (warp != kWarpMma) __syncwarp();
         if (lane == 0) mbar_arrive(&bars.w_empty[s]);
         return w.head >= 0;
     };
@@ -523,136 +530,176 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             __syncwarp();
         } else if (warp == kWarpMma) {
-            const uint64_t k_major = smem_desc(0, 16, 1024, kSwizzle128B);
-            const uint64_t mn_major = smem_desc(0, kSlab, 1024, kSwizzle128B);
-            const uint32_t aQ = smem_u32(sQ), aKV = smem_u32(sKV);
-            const int q_steps = (P.d + 15) / 16, d16 = q_steps * 16;
-            const uint32_t id_s = pa_idesc<T>(kKeys, false), id_o = pa_idesc<T>(d16, true);
-            const bool lead = lane == 0;
-            int g = 0, it = 0;
-            int np[2] = {0, 0};   // P tiles consumed, per tile
-            int no[2] = {0, 0};   // items finished, per tile
-            bool ok = true;
-            PaWork w;
+            if (lane == 0) {
+                const uint64_t k_major = smem_desc(0, 16, 1024, kSwizzle128B);
+                const uint64_t mn_major = smem_desc(0, kSlab, 1024, kSwizzle128B);
+                const uint32_t aQ = smem_u32(sQ) >> 4, aKV = smem_u32(sKV) >> 4;
+                const int q_steps = (P.d + 15) / 16;
+                const uint32_t id_s = pa_idesc<T>(kKeys, false), id_o = pa_idesc<T>(q_steps * 16, true);
+                int g = 0, it = 0;
+                int np0 = 0, np1 = 0;  // P tiles consumed of either tile
+                int no0 = 0, no1 = 0;  // outputs finished
+                int asked = 0, fixed = 0;  // part tiles of V
+                bool ok = true;
+                PaWork w{};
 
-            const auto kv_wait = [&](int idx) {
-                const int st = idx % G::STAGES, use = idx / G::STAGES;
-                ok = ok && __all_sync(~0u, mbar_wait(&bars.kv_full[st], use & 1, wc, kStatusTimeoutLoad,
-                                                     &abort_flag, false));
-                return st;
-            };
-            const auto kv_free = [&](int st) {
-                if (lead) mma_commit(&bars.kv_empty[st]);
-            };
-            // S of tile x = Q (tile qx) K^T
-            const auto qk = [&](int x, int qx, int st) {
-                if (lead) {
-                    for (int kk = 0; kk < q_steps; ++kk) {
-                        const uint32_t off = (kk >> 2) * kSlab + (kk & 3) * 32;
-                        mma_bf16_ss(tmem + x * 128, k_major | ((aQ + qx * G::TILE + off) >> 4),
-                                    k_major | ((aKV + st * G::TILE + off) >> 4), id_s, kk > 0);
+                const auto kv_wait = [&](int idx) {
+                    const int st = idx % G::STAGES, use = idx / G::STAGES;
+                    ok = ok && mbar_wait(&bars.kv_full[st], use & 1, wc, kStatusTimeoutLoad, &abort_flag,
+                                         false);
+                    return st;
+                };
+                // S of tile x = Q (tile qx) K^T
+                const auto qk = [&](int x, int qx, int st) {
+                    const uint64_t da = k_major | (aQ + qx * (G::TILE >> 4));
+                    const uint64_t db = k_major | (aKV + st * (G::TILE >> 4));
+                    const uint32_t dS = tmem + x * 128;
+                    if (q_steps == D / 16) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
+                            mma_bf16_ss(dS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
+                        }
+                    } else {  // channels past d are zero in shared memory: left out
+#pragma unroll 1
+                        for (int kk = 0; kk < q_steps; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
+                            mma_bf16_ss(dS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
+                        }
                     }
                     mma_commit(&bars.s_full[x]);
-                }
-            };
-            // 16-key steps of key tile kt of the sequence that hold keys (at
-            // least one); V rows of the last one behind the sequence become zero
-            const auto steps_of = [&](int kt, int st) {
-                const int left = w.nk - kt * kKeys;
-                if (left >= kKeys) return kKeys / 16;
-                const int keys = max(left, 0), steps = max((keys + 15) / 16, 1);
-                for (int sl = 0; sl < G::SLABS; ++sl)
-                    for (int i = keys * 8 + lane; i < steps * 128; i += 32)
-                        st_shared_v4(aKV + st * G::TILE + sl * kSlab + i * 16, 0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                return steps;
-            };
-            const auto pv = [&](int x, int st, int steps, bool first) {
-                if (!ok) return;
-                ok = __all_sync(~0u, mbar_wait(&bars.p_full[x], np[x] & 1, wc, kStatusTimeoutSync,
-                                               &abort_flag, false));
-                ++np[x];
-                if (first)
-                    ok = ok && __all_sync(~0u, mbar_wait(&bars.o_empty[x], (no[x] & 1) ^ 1, wc,
-                                                         kStatusTimeoutSync, &abort_flag, false));
-                if (!ok) return;
-                tc_fence_after();
-                if (lead)
-                    for (int kk = 0; kk < steps; ++kk)
-                        mma_bf16_ts(tmem + 256 + x * D, tmem + x * 128 + kk * 8,
-                                    mn_major | ((aKV + st * G::TILE + kk * 2048) >> 4), id_o,
-                                    kk > 0 || !first);
-            };
-            const auto finish = [&](int x) {
-                if (lead) mma_commit(&bars.o_full[x]);
-                ++no[x];
-            };
-            for (; ok && next_work(w); ++it) {
-                ok = ok && __all_sync(~0u, mbar_wait(&bars.q_full, it & 1, wc, kStatusTimeoutLoad,
-                                                     &abort_flag, false));
-                if (!ok) break;
-                tc_fence_after();
-                const int n = max(w.n0, w.n1);
-                int st = kv_wait(g);
-                if (!ok) break;
-                if constexpr (!SPLIT) {
-                    if (w.n0 > 0) qk(0, 0, st);
-                    if (w.n1 > 0) qk(1, 1, st);
-                    kv_free(st);
-                    for (int j = 0; ok && j < n; ++j) {
-                        const bool more = j + 1 < n;
-                        const int sk = more ? kv_wait(g + 2 * j + 1) : 0;
-                        const int sv = kv_wait(g + 2 * j + (more ? 2 : 1));
-                        if (!ok) break;
-                        const int steps = steps_of(j, sv);
-                        for (int x = 0; x < 2; ++x) {
-                            const int nx = x ? w.n1 : w.n0;
-                            if (j >= nx) continue;
-                            pv(x, sv, steps, j == 0);
-                            if (!ok) break;
-                            if (j + 1 < nx)
-                                qk(x, x, sk);
-                            else
-                                finish(x);
-                        }
-                        if (!ok) break;
-                        if (more) kv_free(sk);
-                        kv_free(sv);
-                        if (j == n - 2 || n == 1)
-                            if (lead) mma_commit(&bars.q_empty);
+                };
+                // O of tile x (+)= P V; a part tile of V once it is fixed
+                const auto pv = [&](int x, int st, int steps, bool first) {
+                    const int np = x ? np1 : np0, no = x ? no1 : no0;
+                    ok = ok && mbar_wait(&bars.p_full[x], np & 1, wc, kStatusTimeoutSync, &abort_flag, false);
+                    if (asked > fixed) {
+                        ok = ok && mbar_wait(&bars.v_fixed, fixed & 1, wc, kStatusTimeoutSync, &abort_flag,
+                                             false);
+                        ++fixed;
                     }
-                } else {
-                    qk(0, 0, st);
-                    kv_free(st);
-                    for (int j = 0; ok && j < n; ++j) {
-                        const int x = j & 1;
-                        if (j + 1 < n) {
-                            const int sk = kv_wait(g + 2 * j + 1);
-                            if (!ok) break;
-                            // tile x ^ 1's scores are free once its last P V is issued
-                            qk(x ^ 1, 0, sk);
-                            kv_free(sk);
-                        }
-                        if (j + 2 >= n && (j + 1 < n || n == 1))
-                            if (lead) mma_commit(&bars.q_empty);
-                        const int sv = kv_wait(g + 2 * j + (j + 1 < n ? 2 : 1));
-                        if (!ok) break;
-                        const int steps = steps_of(w.lo + j, sv);
-                        pv(x, sv, steps, j < 2);
-                        if (!ok) break;
-                        kv_free(sv);
-                        if (j + 2 >= n) finish(x);
+                    if (first)
+                        ok = ok && mbar_wait(&bars.o_empty[x], (no & 1) ^ 1, wc, kStatusTimeoutSync,
+                                             &abort_flag, false);
+                    if (!ok) return;
+                    if (x) ++np1; else ++np0;
+                    tc_fence_after();
+                    const uint64_t db = mn_major | (aKV + st * (G::TILE >> 4));
+                    const uint32_t dO = tmem + 256 + x * D, aP = tmem + x * 128;
+                    const uint32_t acc = first ? 0u : 1u;
+                    if (steps == kKeys / 16) {
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            mma_bf16_ts(dO, aP + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < steps; ++kk)
+                            mma_bf16_ts(dO, aP + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
                     }
+                };
+                const auto finish = [&](int x) {
+                    mma_commit(&bars.o_full[x]);
+                    if (x) ++no1; else ++no0;
+                };
+                // 16-key steps of key tile kt that hold keys (V has landed); the
+                // next warp is asked to zero a part tile's rows behind the sequence
+                const auto steps_of = [&](int kt) {
+                    const int left = w.nk - kt * kKeys;
+                    if (left >= kKeys) return kKeys / 16;
+                    if (ok) mbar_arrive(&bars.v_ask);
+                    ++asked;
+                    return max((left + 15) / 16, 1);
+                };
+
+                while (ok && next_work(w)) {
+                    ok = mbar_wait(&bars.q_full, it & 1, wc, kStatusTimeoutLoad, &abort_flag, false);
+                    const int n = max(w.n0, w.n1);
+                    int st = kv_wait(g);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if constexpr (!SPLIT) {
+                        qk(0, 0, st);
+                        if (w.n1 > 0) qk(1, 1, st);
+                        mma_commit(&bars.kv_empty[st]);
+                        for (int j = 0; j < n; ++j) {
+                            const bool more = j + 1 < n;
+                            const int sk = more ? kv_wait(g + 2 * j + 1) : 0;
+                            const int sv = kv_wait(g + 2 * j + (more ? 2 : 1));
+                            const int steps = steps_of(j);
+                            if (!ok) break;
+                            if (j < w.n0) {
+                                pv(0, sv, steps, j == 0);
+                                if (!ok) break;
+                                if (j + 1 < w.n0)
+                                    qk(0, 0, sk);
+                                else
+                                    finish(0);
+                            }
+                            if (j < w.n1) {
+                                pv(1, sv, steps, j == 0);
+                                if (!ok) break;
+                                if (j + 1 < w.n1)
+                                    qk(1, 1, sk);
+                                else
+                                    finish(1);
+                            }
+                            if (more) mma_commit(&bars.kv_empty[sk]);
+                            mma_commit(&bars.kv_empty[sv]);
+                            if (j == n - 2 || n == 1) mma_commit(&bars.q_empty);
+                        }
+                    } else {
+                        qk(0, 0, st);
+                        mma_commit(&bars.kv_empty[st]);
+                        for (int j = 0; j < n; ++j) {
+                            const int x = j & 1;
+                            if (j + 1 < n) {
+                                const int sk = kv_wait(g + 2 * j + 1);
+                                if (!ok) break;
+                                // tile x ^ 1's scores are free once its last P V is issued
+                                qk(x ^ 1, 0, sk);
+                                mma_commit(&bars.kv_empty[sk]);
+                            }
+                            if (j == n - 2 || n == 1) mma_commit(&bars.q_empty);
+                            const int sv = kv_wait(g + 2 * j + (j + 1 < n ? 2 : 1));
+                            const int steps = steps_of(w.lo + j);
+                            if (!ok) break;
+                            pv(x, sv, steps, j < 2);
+                            if (!ok) break;
+                            mma_commit(&bars.kv_empty[sv]);
+                            if (j + 2 >= n) finish(x);
+                        }
+                    }
+                    g += 2 * n;
+                    ++it;
                 }
-                g += 2 * n;
-            }
-            // drain: a last commit completes after every product issued here
-            if (lead) {
+                // drain: a last commit completes after every product issued here
                 mma_commit(&bars.fin);
                 mbar_wait(&bars.fin, 0, drain, kStatusTimeoutDrain, nullptr);
             }
             __syncwarp();
+        } else {
+            // Zeroes, when asked, a part tile's V rows behind the sequence in the
+            // last 16-key step that the product reads.
+            PaWork w;
+            int g = 0, asked = 0;
+            bool ok = true;
+            while (ok && next_work(w)) {
+                const int n = max(w.n0, w.n1), kt = w.lo + n - 1;
+                const int keys = max(w.nk - kt * kKeys, 0);
+                g += 2 * n;
+                if (keys >= kKeys) continue;
+                ok = __all_sync(~0u, mbar_wait(&bars.v_ask, asked & 1, wc, kStatusTimeoutSync, &abort_flag));
+                if (!ok) break;
+                ++asked;
+                uint8_t *dst = sKV + (g - 1) % G::STAGES * G::TILE;
+                const int end = max((keys + 15) / 16, 1) * 16;
+                for (int sl = 0; sl < G::SLABS; ++sl)
+                    for (int i = keys * 8 + lane; i < end * 8; i += 32)
+                        st_shared_v4(smem_u32(dst) + sl * kSlab + i * 16, 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.v_fixed);
+            }
         }
     } else {
         regs_alloc<kPaRegsSoftmax>();
