@@ -13,7 +13,7 @@ namespace {
 
 // How a call is split, from sizes that the host knows.
 struct Plan {
-    bool pieces;
+    int kind;  // 0 whole items, 1 pieces of two tiles, 2 pieces of one
     int ctas, tile_tokens, ws_rows;
     int64_t max_items;
     size_t ml_at, o_at, bytes;  // workspace offsets and size (pieces)
@@ -25,22 +25,23 @@ Plan make_plan(int64_t total_q, int64_t total_k, int batch, int heads_q, int hea
     Plan p{};
     const int group = heads_q / heads_kv, sms = sm_count();
     p.tile_tokens = 128 / group;
-    // tiles of one and of two times 128 rows: at most one part tile per sequence
-    const int64_t tiles = least(total_q, total_q / p.tile_tokens + batch) * heads_kv;
+    // items of one and of two tiles of 128 rows: at most one part per sequence
+    const int64_t ones = least(total_q, total_q / p.tile_tokens + batch) * heads_kv;
     const int64_t pairs = least(total_q, total_q / (2 * p.tile_tokens) + batch) * heads_kv;
-    // Pieces where whole items would leave SMs idle and keys are long enough
-    // to share out, and where a sequence's queries fill less than one tile and
-    // its keys outnumber them (the second warpgroup would have nothing to do).
-    const bool few = pairs < 2 * sms && total_k >= 512 * static_cast<int64_t>(batch);
+    // One tile where a sequence's queries fill half of one at most and its keys
+    // outnumber them (a second tile would have nothing to do); two tiles, in
+    // pieces, where whole items would leave SMs idle and keys are long enough
+    // to share out.
     const bool thin = total_q <= static_cast<int64_t>(batch) * p.tile_tokens / 2 && total_k >= 4 * total_q;
-    p.pieces = few || thin;
-    p.ctas = static_cast<int>(p.pieces ? sms : least(pairs, sms));
-    if (!p.pieces) return p;
-    p.max_items = tiles;
+    const bool few = pairs < 2 * sms && total_k >= 512 * static_cast<int64_t>(batch);
+    p.kind = thin ? 2 : few ? 1 : 0;
+    p.ctas = static_cast<int>(p.kind ? sms : least(pairs, sms));
+    if (!p.kind) return p;
+    p.max_items = thin ? ones : pairs;
     p.ws_rows = static_cast<int>(least(128, group * least(p.tile_tokens, total_q)));
     const int D = d <= 64 ? 64 : 128;
-    const size_t rows = static_cast<size_t>(tiles + p.ctas) * 2 * p.ws_rows;
-    p.ml_at = 64 + static_cast<size_t>(tiles) * 32;
+    const size_t rows = static_cast<size_t>(p.max_items + p.ctas) * 2 * p.ws_rows;
+    p.ml_at = 64 + static_cast<size_t>(p.max_items) * 32;
     p.o_at = (p.ml_at + rows * sizeof(float2) + 127) & ~static_cast<size_t>(127);
     p.bytes = p.o_at + rows * D * sizeof(float);
     return p;
@@ -122,7 +123,7 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     const Plan p = make_plan(total_q, total_k, batch, heads_q, heads_kv, d);
     if (p.bytes > 0 && (workspace == nullptr || !aligned(workspace, 128) || workspace_bytes < p.bytes))
         return RPE_ERR_INVALID_ARG;
-    if (p.max_items * p.ws_rows > INT32_MAX) return RPE_ERR_UNSUPPORTED;
+    if (2 * p.max_items * p.ws_rows > INT32_MAX) return RPE_ERR_UNSUPPORTED;
 
     PackedAttnArgs a{};
     a.cu_q = cu_q;
@@ -141,7 +142,7 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     a.out_token = total_q > 1 ? out->token_stride : 0;
     a.out_head = heads_q > 1 ? out->head_stride : 0;
     a.lse = lse;
-    if (p.pieces) {
+    if (p.kind) {
         char *ws = static_cast<char *>(workspace);
         a.workspace = ws;
         a.ws_ml = reinterpret_cast<float2 *>(ws + p.ml_at);
@@ -163,8 +164,8 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     a.status = device_status_word();
     if (a.status == nullptr) return RPE_ERR_CUDA;
     const bool bf16 = dtype == RPE_DTYPE_BF16;
-    const cudaError_t err = d <= 64 ? launch_packed_attn_d64(m, a, bf16, p.pieces, p.ctas, st)
-                                    : launch_packed_attn_d128(m, a, bf16, p.pieces, p.ctas, st);
+    const cudaError_t err = d <= 64 ? launch_packed_attn_d64(m, a, bf16, p.kind, p.ctas, st)
+                                    : launch_packed_attn_d128(m, a, bf16, p.kind, p.ctas, st);
     return err == cudaSuccess ? RPE_OK : RPE_ERR_CUDA;
 }
 

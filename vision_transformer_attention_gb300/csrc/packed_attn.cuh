@@ -7,16 +7,21 @@
 //
 // Tiles. The g query heads that share a key/value head sit side by side in
 // memory, so a tile of 128 rows holds TQ = 128 / g tokens x g heads (one TMA
-// box), and every key tile (128 keys) is read once for all of them. Two such
-// tiles are worked on at a time, each by one softmax warpgroup, one thread per
-// row, while one warp issues the tensor-core products of both in turn, so that
-// one tile's softmax runs under the other's products:
-//   whole items (SPLIT = false): two neighbouring tiles of one sequence and
-//     key/value head, sharing every key tile;
-//   pieces (SPLIT = true; few rows, long keys): one tile against a run of key
-//     tiles, the warpgroups taking every other key tile of it. The unnormalised
-//     outputs go to the caller's workspace in fp32 and packed_combine_kernel
-//     joins them. A CTA's runs are its equal share of all key tiles.
+// box), and every key tile (128 keys) is read once for all of them. A CTA works
+// on two such tiles at a time, each with its own softmax warpgroup, one thread
+// per row, and its own issuing thread for the tensor-core products, so that one
+// tile's softmax and waits run under the other's products (with one issuing
+// thread for both the tensor pipe stood still during its waits: 1.08 instead of
+// XXXX PFLOP/s on long causal prompts). Three kinds of work:
+//   whole (kWhole): two neighbouring tiles of one sequence and key/value head,
+//     sharing every key tile, all keys;
+//   shared (kShared; too few items to fill the GPU): the same against a run of
+//     the key tiles;
+//   alternate (kAlternate; rows for one tile at most): one tile against a run
+//     of key tiles, the warpgroups taking every other key tile of it.
+// In the last two a CTA's runs are its equal share of all key tiles, the
+// unnormalised outputs go to the caller's workspace in fp32, and
+// packed_combine_kernel joins them.
 //
 // Per key tile and tile: S = Q K^T into tensor memory (fp32), the row's 128
 // scores into registers, the running maximum, p = 2^(scale log2e (s - m)) in
@@ -42,10 +47,11 @@
 namespace vta {
 namespace {
 
-constexpr int kPaThreads = 384;  // two softmax warpgroups, then loads, products, schedule, V tails
+constexpr int kPaThreads = 384;  // two softmax warpgroups, then loads, products (2), schedule
 constexpr int kPaRegsControl = 80, kPaRegsSoftmax = 208, kPaRegsLaunch = 168;
 static_assert(128 * kPaRegsControl + 256 * kPaRegsSoftmax <= kPaThreads * kPaRegsLaunch, "register split");
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 10;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 11;  // kWarpMma + tile
+enum { kWhole = 0, kShared = 1, kAlternate = 2 };
 constexpr int kWorkSlots = 3;
 constexpr int kKeys = 128;  // keys per tile
 constexpr float kPaRescaleLog2 = 8.f;
@@ -66,17 +72,17 @@ struct PaWork {
     int head;   // key/value head; -1: no more work
     int k_row, nk;  // the sequence's keys
     int lim0;   // keys that the first token sees (causal; may be <= 0)
-    int lo;     // first key tile
-    int n0, n1; // key tiles of the two tiles (pieces: n0 in all)
-    int slot;   // pieces: where the unnormalised output goes
+    int lo, n;  // key tiles lo .. lo + n - 1
+    int n0, n1; // of them, how many the two tiles need (alternate: not used)
+    int slot;   // shared, alternate: where the unnormalised output goes
 };
 
 struct PaBars {
     uint64_t q_full, q_empty;
     uint64_t kv_full[10], kv_empty[10];
-    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
     uint64_t w_full[kWorkSlots], w_empty[kWorkSlots];
-    uint64_t v_ask, v_fixed, fin;
+    uint64_t turn[2], fin[2];
 };
 
 struct PaSeq {
@@ -224,6 +230,7 @@ __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRin
                 w.lo = 0;
                 w.n0 = pa_tiles(P, q_seq, min(q_seq.nq, tok + P.tile_tokens) - 1);
                 w.n1 = w.toks > P.tile_tokens ? pa_tiles(P, q_seq, min(q_seq.nq, tok + TT) - 1) : 0;
+                w.n = max(w.n0, w.n1);
                 w.slot = 0;
                 alive = ring.put(w, lane);
                 ++round;
@@ -239,24 +246,24 @@ __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRin
     }
 }
 
-// Units (key tiles of one tile and key/value head) and tiles of a sequence.
-__device__ __forceinline__ void pa_units(const PackedAttnArgs &P, const PaSeq &s, long long *units,
-                                         int *tiles) {
+// Units (key tiles of one item) and items of a sequence; an item is TT tokens
+// of one key/value head.
+__device__ __forceinline__ void pa_units(const PackedAttnArgs &P, const PaSeq &s, int TT,
+                                         long long *units, int *items) {
     long long u = 0;
-    const int nt = (s.nq + P.tile_tokens - 1) / P.tile_tokens;
+    const int nt = (s.nq + TT - 1) / TT;
     if (!P.causal || nt <= 1)
         u = static_cast<long long>(nt) * (nt ? pa_tiles(P, s, s.nq - 1) : 0);
     else
-        for (int t = 0; t < nt; ++t)
-            u += pa_tiles(P, s, min(s.nq, (t + 1) * P.tile_tokens) - 1);
+        for (int t = 0; t < nt; ++t) u += pa_tiles(P, s, min(s.nq, (t + 1) * TT) - 1);
     *units = u * P.heads_kv;
-    *tiles = nt * P.heads_kv;
+    *items = nt * P.heads_kv;
 }
 
-// Pieces: this CTA's share [u0, u1) of all units, in (sequence, tile, head,
-// key tile) order. per: sequences per warp of the count before.
+// Shared and alternate: this CTA's share [u0, u1) of all units, in (sequence,
+// tokens, head, key tile) order. per: sequences per warp of the count before.
 __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRing ring, int lane,
-                                                   const long long *warp_units,
+                                                   int TT, const long long *warp_units,
                                                    const int *warp_tiles, int per) {
     long long all = 0;
     int tiles_all = 0;
@@ -298,7 +305,7 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
             s = PaSeq{0, 0, 0, 0};
             if (b + lane < P.batch) {
                 s = pa_seq(P, b + lane, &bad);
-                pa_units(P, s, &u, &n);
+                pa_units(P, s, TT, &u, &n);
             }
             const long long us = warp_scan(u, lane);
             const int ns = warp_scan(n, lane);
@@ -323,10 +330,10 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
     long long u = u0;
     int4 *meta = reinterpret_cast<int4 *>(header + 16);
     for (int t = 0; u < u1;) {
-        const int last = min(s.nq, (t + 1) * P.tile_tokens) - 1;
+        const int last = min(s.nq, (t + 1) * TT) - 1;
         const int kt = pa_tiles(P, s, last);
         const long long span = static_cast<long long>(kt) * P.heads_kv;
-        if (t * P.tile_tokens >= s.nq) {  // next sequence
+        if (t * TT >= s.nq) {  // next sequence
             ++b;
             t = 0;
             if (b >= P.batch) break;
@@ -343,17 +350,19 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
         const long long first = base + static_cast<long long>(h) * kt;  // the item's first unit
         const int lo = static_cast<int>(u - first);
         const int n = static_cast<int>(u1 - u < kt - lo ? u1 - u : kt - lo);
-        const int tok = t * P.tile_tokens;
+        const int tok = t * TT;
         PaWork w;
         w.q_tok = s.q0 + tok;
-        w.toks = min(s.nq - tok, P.tile_tokens);
+        w.toks = min(s.nq - tok, TT);
         w.head = h;
         w.k_row = s.k0;
         w.nk = s.nk;
         w.lim0 = tok + 1 + s.nk - s.nq;
         w.lo = lo;
-        w.n0 = n;
-        w.n1 = 0;
+        w.n = n;
+        const int kt0 = pa_tiles(P, s, min(s.nq, tok + P.tile_tokens) - 1);
+        w.n0 = min(max(kt0 - lo, 0), n);
+        w.n1 = w.toks > P.tile_tokens ? n : 0;
         w.slot = item + h + blockIdx.x;
         if (lo == 0 && lane == 0) {
             meta[2 * (item + h)] = make_int4(static_cast<int>(first & 0xFFFFFFFFll),
@@ -368,11 +377,12 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
 
 // ------------------------------------------------------------- the kernel
 
-template <typename T, int D, bool SPLIT>
+template <typename T, int D, int KIND>
 __global__ void __launch_bounds__(kPaThreads, 1)
 packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PackedAttnArgs P) {
     using G = PaGeo<D>;
+    constexpr bool ALT = KIND == kAlternate, PIECES = KIND != kWhole;
     extern __shared__ __align__(1024) uint8_t pa_smem[];
     __shared__ PaBars bars;
     __shared__ PaWork work[kWorkSlots];
@@ -388,13 +398,14 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     if (tid == 0) {
         mbar_init(&bars.q_full, 1);
-        mbar_init(&bars.q_empty, 1);
+        mbar_init(&bars.q_empty, 2);  // one arrival per issuing thread
         for (int i = 0; i < G::STAGES; ++i) {
             mbar_init(&bars.kv_full[i], 1);
-            mbar_init(&bars.kv_empty[i], 1);
+            mbar_init(&bars.kv_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_half[i], 4);
             mbar_init(&bars.p_full[i], 4);
             mbar_init(&bars.o_full[i], 1);
             mbar_init(&bars.o_empty[i], 4);
@@ -403,9 +414,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_init(&bars.w_full[i], 1);
             mbar_init(&bars.w_empty[i], 11);
         }
-        mbar_init(&bars.v_ask, 1);
-        mbar_init(&bars.v_fixed, 1);
-        mbar_init(&bars.fin, 1);
+        mbar_init(&bars.turn[0], 1);
+        mbar_init(&bars.turn[1], 1);
+        mbar_init(&bars.fin[0], 1);
+        mbar_init(&bars.fin[1], 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -415,6 +427,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // Count before the roles part: units and tiles (pieces) or the most key
     // tiles of a sequence (whole items), each warp over its run of sequences.
     const int per = (P.batch + kPaThreads - 1) / kPaThreads * 32;
+    const int TT = (ALT ? 1 : 2) * P.tile_tokens;
     {
         bool bad = false;
         long long units = 0;
@@ -423,10 +436,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int b = warp * per + i + lane;
             if (b >= P.batch) continue;
             const PaSeq s = pa_seq(P, b, &bad);
-            if constexpr (SPLIT) {
+            if constexpr (PIECES) {
                 long long u;
                 int n;
-                pa_units(P, s, &u, &n);
+                pa_units(P, s, TT, &u, &n);
                 units += u;
                 tiles += n;
             } else {
@@ -434,7 +447,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
         if (bad) atomicOr(P.status, kStatusBadSequence);
-        if constexpr (SPLIT) {
+        if constexpr (PIECES) {
             units = warp_sum64(units);
             tiles = warp_sum(tiles);
         } else {
@@ -452,18 +465,19 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     // The next entry of the schedule; every role walks the same list (a whole
     // warp, or for the products its first lane).
+    const bool one_lane = warp == kWarpMma || warp == kWarpMma + 1;
     int wn = 0;
     const auto next_work = [&](PaWork &w) -> bool {
         const int s = wn % kWorkSlots, use = wn / kWorkSlots;
         ++wn;
-        const bool ok = mbar_wait(&bars.w_full[s], use & 1, wc, kStatusTimeoutSync, &abort_flag);
-        if (warp == kWarpMma) {
+        const bool ok = mbar_wait(&bars.w_full[s], use & 1, wc, kStatusTimeoutSync, &abort_flag, false);
+        if (one_lane) {
             if (!ok) return false;
         } else if (!__all_sync(~0u, ok)) {
             return false;
         }
         w = work[s];
-        if (warp != kWarpMma) __syncwarp();
+        if (!one_lane) __syncwarp();
         if (lane == 0) mbar_arrive(&bars.w_empty[s]);
         return w.head >= 0;
     };
@@ -472,8 +486,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         regs_dealloc<kPaRegsControl>();
         if (warp == kWarpSched) {
             PaRing ring{work, bars.w_full, bars.w_empty, &wc, &abort_flag};
-            if constexpr (SPLIT) {
-                pa_schedule_pieces(P, ring, lane, warp_units, warp_tiles, per);
+            if constexpr (PIECES) {
+                pa_schedule_pieces(P, ring, lane, TT, warp_units, warp_tiles, per);
             } else {
                 int most = 1;
                 for (int i = 0; i < kPaThreads / 32; ++i) most = max(most, warp_tiles[i]);
@@ -491,9 +505,9 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             PaWork w;
             for (; ok && next_work(w); ++it) {
                 ok = __all_sync(~0u, mbar_wait(&bars.q_empty, (it & 1) ^ 1, wc, kStatusTimeoutSync,
-                                               &abort_flag));
+                                               &abort_flag, false));
                 if (!ok) break;
-                const int tiles_q = SPLIT ? 1 : (w.n1 > 0 ? 2 : 1);
+                const int tiles_q = !ALT && w.n1 > 0 ? 2 : 1;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bars.q_full, tiles_q * q_bytes);
                     for (int i = 0; i < tiles_q; ++i)
@@ -501,21 +515,18 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             tma_load_3d(sQ + i * G::TILE + sl * kSlab, &tm_q, &bars.q_full, sl * 64,
                                         w.head * P.group, w.q_tok + i * P.tile_tokens);
                 }
-                const int n = max(w.n0, w.n1);
-                // K0, then K(j + 1), V(j): the order in which they are used
-                for (int j = 0; j < 2 * n; ++j, ++g) {
-                    const bool is_k = j == 0 || ((j & 1) != 0 && j < 2 * n - 1);
-                    const int kt = is_k ? (j + 1) / 2 : (j == 2 * n - 1 ? n - 1 : j / 2 - 1);
+                for (int j = 0; j < 2 * w.n; ++j, ++g) {  // K0 V0 K1 V1 ...
+                    const bool is_k = (j & 1) == 0;
                     const int st = g % G::STAGES, use = g / G::STAGES;
                     ok = __all_sync(~0u, mbar_wait(&bars.kv_empty[st], (use & 1) ^ 1, wc,
-                                                   kStatusTimeoutSync, &abort_flag));
+                                                   kStatusTimeoutSync, &abort_flag, false));
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bars.kv_full[st], G::TILE);
                         for (int sl = 0; sl < G::SLABS; ++sl)
                             tma_load_3d(sKV + st * G::TILE + sl * kSlab, is_k ? &tm_k : &tm_v,
                                         &bars.kv_full[st], sl * 64, w.head,
-                                        w.k_row + (w.lo + kt) * kKeys);
+                                        w.k_row + (w.lo + j / 2) * kKeys);
                     }
                 }
             }
@@ -529,178 +540,164 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             __syncwarp();
-        } else if (warp == kWarpMma) {
-            if (lane == 0) {
-                const uint64_t k_major = smem_desc(0, 16, 1024, kSwizzle128B);
-                const uint64_t mn_major = smem_desc(0, kSlab, 1024, kSwizzle128B);
-                const uint32_t aQ = smem_u32(sQ) >> 4, aKV = smem_u32(sKV) >> 4;
-                const int q_steps = (P.d + 15) / 16;
-                const uint32_t id_s = pa_idesc<T>(kKeys, false), id_o = pa_idesc<T>(q_steps * 16, true);
-                int g = 0, it = 0;
-                int np0 = 0, np1 = 0;  // P tiles consumed of either tile
-                int no0 = 0, no1 = 0;  // outputs finished
-                int asked = 0, fixed = 0;  // part tiles of V
-                bool ok = true;
-                PaWork w{};
-
-                const auto kv_wait = [&](int idx) {
-                    const int st = idx % G::STAGES, use = idx / G::STAGES;
-                    ok = ok && mbar_wait(&bars.kv_full[st], use & 1, wc, kStatusTimeoutLoad, &abort_flag,
-                                         false);
-                    return st;
-                };
-                // S of tile x = Q (tile qx) K^T
-                const auto qk = [&](int x, int qx, int st) {
-                    const uint64_t da = k_major | (aQ + qx * (G::TILE >> 4));
-                    const uint64_t db = k_major | (aKV + st * (G::TILE >> 4));
-                    const uint32_t dS = tmem + x * 128;
-                    if (q_steps == D / 16) {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
-                            mma_bf16_ss(dS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
-                        }
-                    } else {  // channels past d are zero in shared memory: left out
-#pragma unroll 1
-                        for (int kk = 0; kk < q_steps; ++kk) {
-                            const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
-                            mma_bf16_ss(dS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
-                        }
-                    }
-                    mma_commit(&bars.s_full[x]);
-                };
-                // O of tile x (+)= P V; a part tile of V once it is fixed
-                const auto pv = [&](int x, int st, int steps, bool first) {
-                    const int np = x ? np1 : np0, no = x ? no1 : no0;
-                    ok = ok && mbar_wait(&bars.p_full[x], np & 1, wc, kStatusTimeoutSync, &abort_flag, false);
-                    if (asked > fixed) {
-                        ok = ok && mbar_wait(&bars.v_fixed, fixed & 1, wc, kStatusTimeoutSync, &abort_flag,
-                                             false);
-                        ++fixed;
-                    }
-                    if (first)
-                        ok = ok && mbar_wait(&bars.o_empty[x], (no & 1) ^ 1, wc, kStatusTimeoutSync,
-                                             &abort_flag, false);
-                    if (!ok) return;
-                    if (x) ++np1; else ++np0;
-                    tc_fence_after();
-                    const uint64_t db = mn_major | (aKV + st * (G::TILE >> 4));
-                    const uint32_t dO = tmem + 256 + x * D, aP = tmem + x * 128;
-                    const uint32_t acc = first ? 0u : 1u;
-                    if (steps == kKeys / 16) {
-#pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_bf16_ts(dO, aP + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
-                    } else {
-#pragma unroll 1
-                        for (int kk = 0; kk < steps; ++kk)
-                            mma_bf16_ts(dO, aP + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
-                    }
-                };
-                const auto finish = [&](int x) {
-                    mma_commit(&bars.o_full[x]);
-                    if (x) ++no1; else ++no0;
-                };
-                // 16-key steps of key tile kt that hold keys (V has landed); the
-                // next warp is asked to zero a part tile's rows behind the sequence
-                const auto steps_of = [&](int kt) {
-                    const int left = w.nk - kt * kKeys;
-                    if (left >= kKeys) return kKeys / 16;
-                    if (ok) mbar_arrive(&bars.v_ask);
-                    ++asked;
-                    return max((left + 15) / 16, 1);
-                };
-
-                while (ok && next_work(w)) {
-                    ok = mbar_wait(&bars.q_full, it & 1, wc, kStatusTimeoutLoad, &abort_flag, false);
-                    const int n = max(w.n0, w.n1);
-                    int st = kv_wait(g);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if constexpr (!SPLIT) {
-                        qk(0, 0, st);
-                        if (w.n1 > 0) qk(1, 1, st);
-                        mma_commit(&bars.kv_empty[st]);
-                        for (int j = 0; j < n; ++j) {
-                            const bool more = j + 1 < n;
-                            const int sk = more ? kv_wait(g + 2 * j + 1) : 0;
-                            const int sv = kv_wait(g + 2 * j + (more ? 2 : 1));
-                            const int steps = steps_of(j);
-                            if (!ok) break;
-                            if (j < w.n0) {
-                                pv(0, sv, steps, j == 0);
-                                if (!ok) break;
-                                if (j + 1 < w.n0)
-                                    qk(0, 0, sk);
-                                else
-                                    finish(0);
-                            }
-                            if (j < w.n1) {
-                                pv(1, sv, steps, j == 0);
-                                if (!ok) break;
-                                if (j + 1 < w.n1)
-                                    qk(1, 1, sk);
-                                else
-                                    finish(1);
-                            }
-                            if (more) mma_commit(&bars.kv_empty[sk]);
-                            mma_commit(&bars.kv_empty[sv]);
-                            if (j == n - 2 || n == 1) mma_commit(&bars.q_empty);
-                        }
-                    } else {
-                        qk(0, 0, st);
-                        mma_commit(&bars.kv_empty[st]);
-                        for (int j = 0; j < n; ++j) {
-                            const int x = j & 1;
-                            if (j + 1 < n) {
-                                const int sk = kv_wait(g + 2 * j + 1);
-                                if (!ok) break;
-                                // tile x ^ 1's scores are free once its last P V is issued
-                                qk(x ^ 1, 0, sk);
-                                mma_commit(&bars.kv_empty[sk]);
-                            }
-                            if (j == n - 2 || n == 1) mma_commit(&bars.q_empty);
-                            const int sv = kv_wait(g + 2 * j + (j + 1 < n ? 2 : 1));
-                            const int steps = steps_of(w.lo + j);
-                            if (!ok) break;
-                            pv(x, sv, steps, j < 2);
-                            if (!ok) break;
-                            mma_commit(&bars.kv_empty[sv]);
-                            if (j + 2 >= n) finish(x);
-                        }
-                    }
-                    g += 2 * n;
-                    ++it;
-                }
-                // drain: a last commit completes after every product issued here
-                mma_commit(&bars.fin);
-                mbar_wait(&bars.fin, 0, drain, kStatusTimeoutDrain, nullptr);
-            }
-            __syncwarp();
-        } else {
-            // Zeroes, when asked, a part tile's V rows behind the sequence in the
-            // last 16-key step that the product reads.
-            PaWork w;
-            int g = 0, asked = 0;
+        } else if (lane == 0) {
+            // -------------------------------------------- products of tile x
+            const int x = warp - kWarpMma;
+            const uint64_t k_major = smem_desc(0, 16, 1024, kSwizzle128B);
+            const uint64_t mn_major = smem_desc(0, kSlab, 1024, kSwizzle128B);
+            const uint32_t aQ = (smem_u32(sQ) + (ALT ? 0 : x) * G::TILE) >> 4, aKV = smem_u32(sKV) >> 4;
+            const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * D;
+            const int q_steps = (P.d + 15) / 16;
+            const uint32_t id_s = pa_idesc<T>(kKeys, false), id_o = pa_idesc<T>(q_steps * 16, true);
+            int st = 0, ph = 0;  // stage and parity of the next K or V tile
+            int it = 0, np = 0, no = 0;  // items, P tiles, outputs of this tile
+            int turns = 0;
             bool ok = true;
+            PaWork w{};
+
+            const auto kv_wait = [&]() {
+                ok = ok && mbar_wait(&bars.kv_full[st], ph, wc, kStatusTimeoutLoad, &abort_flag, false);
+                return ok;
+            };
+            // the stage after this one, which is waited for again later
+            const auto kv_peek = [&]() {
+                const int s2 = st + 1 == G::STAGES ? 0 : st + 1;
+                ok = ok && mbar_wait(&bars.kv_full[s2], s2 == 0 ? ph ^ 1 : ph, wc, kStatusTimeoutLoad,
+                                     &abort_flag, false);
+            };
+            // The two threads issue their P V and Q K^T in turn, so that the tiles
+            // stay half a period apart: without it they fall into step, both
+            // softmaxes beside an idle tensor pipe and then both products.
+            const auto take_turn = [&]() {
+                ok = ok && mbar_wait(&bars.turn[x], (turns & 1) ^ (x ^ 1), wc, kStatusTimeoutSync,
+                                     &abort_flag, false);
+                ++turns;
+                return ok;
+            };
+            const auto pass_turn = [&]() { mbar_arrive(&bars.turn[x ^ 1]); };
+            // done with the stage: after the products issued so far, or at once
+            const auto kv_done = [&](bool used) {
+                if (used)
+                    mma_commit(&bars.kv_empty[st]);
+                else
+                    mbar_arrive(&bars.kv_empty[st]);
+                if (++st == G::STAGES) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            };
+            const auto qk = [&]() {  // S = Q K^T
+                const uint64_t da = k_major | aQ, db = k_major | (aKV + st * (G::TILE >> 4));
+                if (q_steps == D / 16) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
+                        mma_bf16_ss(tS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
+                    }
+                } else {  // channels past d are zero in shared memory: left out
+#pragma unroll 1
+                    for (int kk = 0; kk < q_steps; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
+                        mma_bf16_ss(tS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
+                    }
+                }
+                mma_commit(&bars.s_full[x]);
+            };
+            const auto pv = [&](int kt, bool first) {  // O (+)= P V
+                const int left = w.nk - kt * kKeys;
+                const uint64_t db = mn_major | (aKV + st * (G::TILE >> 4));
+                const uint32_t acc = first ? 0u : 1u;
+                ok = mbar_wait(&bars.p_half[x], np & 1, wc, kStatusTimeoutSync, &abort_flag, false);
+                if (ok && first)
+                    ok = mbar_wait(&bars.o_empty[x], (no & 1) ^ 1, wc, kStatusTimeoutSync, &abort_flag, false);
+                if (!ok || (!ALT && !take_turn())) return;
+                tc_fence_after();
+                // the first half of the keys, then the rest once it is written
+                if (left >= kKeys) {
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 32; ++kk)
+                        mma_bf16_ts(tO, tS + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
+                }
+                ok = mbar_wait(&bars.p_full[x], np & 1, wc, kStatusTimeoutSync, &abort_flag, false);
+                ++np;
+                if (!ok) return;
+                tc_fence_after();
+                if (left >= kKeys) {
+#pragma unroll
+                    for (int kk = kKeys / 32; kk < kKeys / 16; ++kk)
+                        mma_bf16_ts(tO, tS + kk * 8, db + kk * (2048 >> 4), id_o, 1u);
+                } else {  // only the 16-key steps that hold keys (one at least)
+                    const int steps = max((left + 15) / 16, 1);
+#pragma unroll 1
+                    for (int kk = 0; kk < steps; ++kk)
+                        mma_bf16_ts(tO, tS + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
+                }
+            };
+
             while (ok && next_work(w)) {
-                const int n = max(w.n0, w.n1), kt = w.lo + n - 1;
-                const int keys = max(w.nk - kt * kKeys, 0);
-                g += 2 * n;
-                if (keys >= kKeys) continue;
-                ok = __all_sync(~0u, mbar_wait(&bars.v_ask, asked & 1, wc, kStatusTimeoutSync, &abort_flag));
-                if (!ok) break;
-                ++asked;
-                uint8_t *dst = sKV + (g - 1) % G::STAGES * G::TILE;
-                const int end = max((keys + 15) / 16, 1) * 16;
-                for (int sl = 0; sl < G::SLABS; ++sl)
-                    for (int i = keys * 8 + lane; i < end * 8; i += 32)
-                        st_shared_v4(smem_u32(dst) + sl * kSlab + i * 16, 0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.v_fixed);
+                ok = mbar_wait(&bars.q_full, it & 1, wc, kStatusTimeoutLoad, &abort_flag, false);
+                ++it;
+                if constexpr (!ALT) {
+                    // S(0); then per key tile: P V, S of the next
+                    const int nx = x ? w.n1 : w.n0;
+                    if (!kv_wait()) break;
+                    tc_fence_after();
+                    if (nx > 0) qk();
+                    kv_done(nx > 0);
+                    if (nx == 0) mbar_arrive(&bars.q_empty);
+                    if (nx == 1) mma_commit(&bars.q_empty);
+                    for (int j = 0; j < w.n; ++j) {
+                        const bool more = j + 1 < w.n;
+                        if (!kv_wait()) break;
+                        if (more) kv_peek();
+                        if (j < nx) {
+                            pv(w.lo + j, j == 0);
+                        } else {
+                            take_turn();
+                        }
+                        if (!ok) break;
+                        kv_done(j < nx);
+                        if (more) {
+                            if (j + 1 < nx) qk();
+                            pass_turn();
+                            kv_done(j + 1 < nx);
+                            if (j + 2 == nx) mma_commit(&bars.q_empty);
+                        } else {
+                            pass_turn();
+                        }
+                        if (j + 1 == nx) {
+                            mma_commit(&bars.o_full[x]);
+                            ++no;
+                        }
+                    }
+                } else {
+                    // this thread's key tiles are x, x + 2, ...; it lets go of the
+                    // others as they land
+                    const int nx = (w.n + 1 - x) / 2;
+                    if (nx == 0) mbar_arrive(&bars.q_empty);
+                    for (int j = 0; j < w.n; ++j) {
+                        const bool mine = (j & 1) == x;
+                        if (!kv_wait()) break;
+                        tc_fence_after();
+                        if (mine) qk();
+                        kv_done(mine);
+                        if (mine && j + 2 >= w.n) mma_commit(&bars.q_empty);
+                        if (!kv_wait()) break;
+                        if (mine) pv(w.lo + j, j < 2);
+                        if (!ok) break;
+                        kv_done(mine);
+                        if (mine && j + 2 >= w.n) {
+                            mma_commit(&bars.o_full[x]);
+                            ++no;
+                        }
+                    }
+                }
             }
+            // drain: a last commit completes after every product issued here
+            mma_commit(&bars.fin[x]);
+            mbar_wait(&bars.fin[x], 0, drain, kStatusTimeoutDrain, nullptr);
         }
+        __syncwarp();
     } else {
         regs_alloc<kPaRegsSoftmax>();
         const int x = warp >> 2;                     // which tile
@@ -709,26 +706,43 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int tok_first = (row & ~31) / P.group; // token of the warp's first row
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field: 32 * warp
         const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * D;
-        int ns = 0, no = 0;
+        int ns = 0, no = 0, g = 0;  // S tiles and outputs of this tile, K and V tiles
         const float c = P.scale_log2;
         const float2 c2 = make_float2(c, c);
         PaWork w;
         bool ok = true;
         while (ok && next_work(w)) {
-            const int n = SPLIT ? (w.n0 + 1 - x) / 2 : (x ? w.n1 : w.n0);
-            const int shift_tok = SPLIT ? 0 : x * P.tile_tokens;
+            const int n = ALT ? (w.n + 1 - x) / 2 : (x ? w.n1 : w.n0);
+            const int shift_tok = ALT ? 0 : x * P.tile_tokens;
             const int toks = min(w.toks - shift_tok, P.tile_tokens);  // of this tile
             const bool valid = tok < toks;
-            int lim = P.causal ? min(w.nk, w.lim0 + shift_tok + tok) : w.nk;
+            const int lim = P.causal ? min(w.nk, w.lim0 + shift_tok + tok) : w.nk;
             // masking is tested per warp against its first row, which sees least
             const int lim_first = P.causal ? min(w.nk, w.lim0 + shift_tok + tok_first) : w.nk;
             const bool warp_live = tok_first < toks && tok_first < P.tile_tokens;
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < n; ++i, ++ns) {
-                const int kt = SPLIT ? w.lo + 2 * i + x : i;
+                const int j = ALT ? 2 * i + x : i, kt = w.lo + j;
                 ok = __all_sync(~0u, mbar_wait(&bars.s_full[x], ns & 1, wc, kStatusTimeoutMma, &abort_flag,
                                                false));
                 if (!ok) break;
+                if (w.nk < (kt + 1) * kKeys) {
+                    // A part tile: V's rows behind the sequence in the last 16-key
+                    // step that the product reads become zero. (Of this stage's
+                    // fills the one before has been used, K behind it having given
+                    // S, and the one after waits for this P V, so the parity is
+                    // unambiguous. Both tiles may do this: they write the same.)
+                    const int idx = g + 2 * j + 1, st = idx % G::STAGES, use = idx / G::STAGES;
+                    ok = __all_sync(~0u, mbar_wait(&bars.kv_full[st], use & 1, wc, kStatusTimeoutLoad,
+                                                   &abort_flag, false));
+                    if (!ok) break;
+                    const int keys = max(w.nk - kt * kKeys, 0), end = max((keys + 15) / 16, 1) * 16;
+                    const uint32_t dst = smem_u32(sKV) + st * G::TILE;
+                    for (int sl = 0; sl < G::SLABS; ++sl)
+                        for (int e = keys * 8 + row; e < end * 8; e += 128)
+                            st_shared_v4(dst + sl * kSlab + e * 16, 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
                 if (warp_live) {
                     tc_fence_after();
                     uint32_t s[4][32];
@@ -796,6 +810,12 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             pk[e] = pa_pack<T>(p.x, p.y);
                         }
                         tmem_st16(tS + q * 16, pk);
+                        if (q == 1) {  // half of the keys: the product may start
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars.p_half[x]);
+                        }
                     }
                     const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
                     l += t.x + t.y;
@@ -803,9 +823,13 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[x]);
+                if (lane == 0) {
+                    if (!warp_live) mbar_arrive(&bars.p_half[x]);
+                    mbar_arrive(&bars.p_full[x]);
+                }
             }
             if (!ok) break;
+            g += 2 * w.n;
             if (n > 0) {
                 ok = __all_sync(~0u, mbar_wait(&bars.o_full[x], no & 1, wc, kStatusTimeoutMma, &abort_flag,
                                                false));
@@ -813,7 +837,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 ++no;
                 tc_fence_after();
             }
-            if constexpr (SPLIT) {
+            if constexpr (PIECES) {
                 const int64_t at = (static_cast<int64_t>(w.slot) * 2 + x) * P.ws_rows + row;
                 const bool mine = valid && row < P.ws_rows;
                 if (mine) P.ws_ml[at] = make_float2(n > 0 ? m : -INFINITY, n > 0 ? l : 0.f);
@@ -882,30 +906,32 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // pieces); otherwise a warp per row.
 constexpr int kJoinWarps = 8;
 
-template <typename T, int D, bool WIDE>
+template <typename T, int D, bool ALT, bool WIDE>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int grid) {
     constexpr int C = D / 32;  // columns per lane
     __shared__ float part[WIDE ? kJoinWarps : 1][WIDE ? D : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int blocks = WIDE ? P.ws_rows : (P.ws_rows + kJoinWarps - 1) / kJoinWarps;
+    const int rows = (ALT ? 1 : 2) * P.ws_rows;  // of an item
+    const int blocks = WIDE ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
     const int item = blockIdx.x / blocks;
-    const int row = WIDE ? blockIdx.x - item * blocks : (blockIdx.x - item * blocks) * kJoinWarps + warp;
+    const int item_row = WIDE ? blockIdx.x - item * blocks : (blockIdx.x - item * blocks) * kJoinWarps + warp;
+    const int x = !ALT && item_row >= P.ws_rows ? 1 : 0, row = item_row - x * P.ws_rows;
     griddep_wait();
     const int *header = static_cast<const int *>(P.workspace);
     const long long all = *reinterpret_cast<const long long *>(header);
-    if (item >= header[2] || row >= P.ws_rows) return;
+    if (item >= header[2] || item_row >= rows) return;
     const int4 *meta = reinterpret_cast<const int4 *>(header + 16) + 2 * item;
     const int4 a = meta[0], b = meta[1];
-    const int tok = row / P.group;
-    if (tok >= b.x) return;
+    const int tile_tok = row / P.group, tok = x * P.tile_tokens + tile_tok;
+    if (tile_tok >= P.tile_tokens || tok >= b.x) return;
     const long long first = (static_cast<long long>(a.y) << 32) | static_cast<uint32_t>(a.x);
     const long long ctas = all < grid ? all : grid;
     const int c0 = static_cast<int>(((first + 1) * ctas - 1) / all);
     const int c1 = static_cast<int>(((first + a.z) * ctas - 1) / all);
-    const int pieces = 2 * (c1 - c0 + 1);
+    const int pieces = (ALT ? 2 : 1) * (c1 - c0 + 1);
     const auto at = [&](int p) {
-        return (static_cast<int64_t>(item + c0) * 2 + p) * P.ws_rows + row;
+        return (static_cast<int64_t>(item + c0) * 2 + (ALT ? p : 2 * p + x)) * P.ws_rows + row;
     };
     float M = -INFINITY;
     for (int p = lane; p < pieces; p += 32) M = fmaxf(M, P.ws_ml[at(p)].x);
@@ -952,7 +978,7 @@ packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int grid) {
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const int64_t token = a.w + tok;
-    const int64_t head = static_cast<int64_t>(b.y) * P.group + (row - tok * P.group);
+    const int64_t head = static_cast<int64_t>(b.y) * P.group + (row - tile_tok * P.group);
     if (lane == 0 && P.lse != nullptr)
         P.lse[token * P.group * P.heads_kv + head] =
             L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
@@ -967,25 +993,37 @@ packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int grid) {
         *reinterpret_cast<uint32_t *>(dst) = pa_pack<T>(acc[0], acc[1]);
 }
 
-template <typename T, int D>
-cudaError_t pa_launch(const PackedAttnMaps &m, const PackedAttnArgs &a, bool pieces, int ctas,
-                      cudaStream_t stream) {
-    void (*kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const PackedAttnArgs) =
-        pieces ? packed_attn_kernel<T, D, true> : packed_attn_kernel<T, D, false>;
+template <typename T, int D, int KIND>
+cudaError_t pa_launch_kind(const PackedAttnMaps &m, const PackedAttnArgs &a, int ctas,
+                           cudaStream_t stream) {
+    auto kernel = packed_attn_kernel<T, D, KIND>;
     cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            PaGeo<D>::SMEM);
     if (err != cudaSuccess) return err;
     err = launch_pdl(kernel, dim3(ctas), dim3(kPaThreads), PaGeo<D>::SMEM, stream, m.q, m.k, m.v, a);
-    if (err != cudaSuccess || !pieces) return err;
-    const int64_t rows = static_cast<int64_t>(a.max_items) * a.ws_rows;
-    if (rows <= 16 * sm_count())
-        return launch_pdl(packed_combine_kernel<T, D, true>, dim3(static_cast<unsigned>(rows)),
-                          dim3(32 * kJoinWarps), 0, stream, a, ctas);
-    const int blocks = (a.ws_rows + kJoinWarps - 1) / kJoinWarps;
-    return launch_pdl(packed_combine_kernel<T, D, false>,
-                      dim3(static_cast<unsigned>(a.max_items) * blocks), dim3(32 * kJoinWarps), 0,
-                      stream, a, ctas);
+    if constexpr (KIND != kWhole) {
+        if (err != cudaSuccess) return err;
+        constexpr bool ALT = KIND == kAlternate;
+        const int rows = (ALT ? 1 : 2) * a.ws_rows;
+        const int64_t all = static_cast<int64_t>(a.max_items) * rows;
+        if (all <= 16 * sm_count())
+            return launch_pdl(packed_combine_kernel<T, D, ALT, true>, dim3(static_cast<unsigned>(all)),
+                              dim3(32 * kJoinWarps), 0, stream, a, ctas);
+        const int blocks = (rows + kJoinWarps - 1) / kJoinWarps;
+        return launch_pdl(packed_combine_kernel<T, D, ALT, false>,
+                          dim3(static_cast<unsigned>(a.max_items) * blocks), dim3(32 * kJoinWarps),
+                          0, stream, a, ctas);
+    }
+    return err;
+}
+
+template <typename T, int D>
+cudaError_t pa_launch(const PackedAttnMaps &m, const PackedAttnArgs &a, int kind, int ctas,
+                      cudaStream_t stream) {
+    return kind == kWhole    ? pa_launch_kind<T, D, kWhole>(m, a, ctas, stream)
+           : kind == kShared ? pa_launch_kind<T, D, kShared>(m, a, ctas, stream)
+                             : pa_launch_kind<T, D, kAlternate>(m, a, ctas, stream);
 }
 
 }  // namespace

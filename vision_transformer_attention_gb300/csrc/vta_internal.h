@@ -187,12 +187,13 @@ struct PackedAttnArgs {
 struct PackedAttnMaps {
     CUtensorMap q, k, v;
 };
-// pieces: the kernel that writes unnormalised pieces on `ctas` CTAs, then the
-// one that joins them; otherwise whole items on `ctas` CTAs. bf16: the type.
+// kind: 0 whole items on `ctas` CTAs; 1, 2 (two tiles that share their keys,
+// one tile with its keys dealt over the warpgroups): the kernel that writes
+// unnormalised pieces, then the one that joins them. bf16: the type.
 cudaError_t launch_packed_attn_d64(const PackedAttnMaps &m, const PackedAttnArgs &a, bool bf16,
-                                   bool pieces, int ctas, cudaStream_t stream);
+                                   int kind, int ctas, cudaStream_t stream);
 cudaError_t launch_packed_attn_d128(const PackedAttnMaps &m, const PackedAttnArgs &a, bool bf16,
-                                    bool pieces, int ctas, cudaStream_t stream);
+                                    int kind, int ctas, cudaStream_t stream);
 
 cudaError_t launch_wait_probe(unsigned long long limit_ns, cudaStream_t stream);
 
