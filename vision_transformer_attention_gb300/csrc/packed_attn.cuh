@@ -80,7 +80,7 @@ struct PaWork {
 struct PaBars {
     uint64_t q_full, q_empty;
     uint64_t kv_full[10], kv_empty[10];
-    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
     uint64_t w_full[kWorkSlots], w_empty[kWorkSlots];
     uint64_t turn[2], fin[2];
 };
@@ -405,7 +405,6 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_half[i], 4);
             mbar_init(&bars.p_full[i], 4);
             mbar_init(&bars.o_full[i], 1);
             mbar_init(&bars.o_empty[i], 4);
@@ -586,13 +585,15 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ph ^= 1;
                 }
             };
-            const auto qk = [&]() {  // S = Q K^T
+            // S = Q K^T; pass: hand the turn over while the last products are issued
+            const auto qk = [&](bool pass) {
                 const uint64_t da = k_major | aQ, db = k_major | (aKV + st * (G::TILE >> 4));
                 if (q_steps == D / 16) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
                         mma_bf16_ss(tS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
+                        if (kk == D / 16 - 3 && pass) pass_turn();
                     }
                 } else {  // channels past d are zero in shared memory: left out
 #pragma unroll 1
@@ -600,6 +601,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
                         mma_bf16_ss(tS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
                     }
+                    if (pass) pass_turn();
                 }
                 mma_commit(&bars.s_full[x]);
             };
@@ -607,25 +609,16 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int left = w.nk - kt * kKeys;
                 const uint64_t db = mn_major | (aKV + st * (G::TILE >> 4));
                 const uint32_t acc = first ? 0u : 1u;
-                ok = mbar_wait(&bars.p_half[x], np & 1, wc, kStatusTimeoutSync, &abort_flag, false);
+                ok = mbar_wait(&bars.p_full[x], np & 1, wc, kStatusTimeoutSync, &abort_flag, false);
+                ++np;
                 if (ok && first)
                     ok = mbar_wait(&bars.o_empty[x], (no & 1) ^ 1, wc, kStatusTimeoutSync, &abort_flag, false);
                 if (!ok || (!ALT && !take_turn())) return;
                 tc_fence_after();
-                // the first half of the keys, then the rest once it is written
                 if (left >= kKeys) {
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 32; ++kk)
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
                         mma_bf16_ts(tO, tS + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
-                }
-                ok = mbar_wait(&bars.p_full[x], np & 1, wc, kStatusTimeoutSync, &abort_flag, false);
-                ++np;
-                if (!ok) return;
-                tc_fence_after();
-                if (left >= kKeys) {
-#pragma unroll
-                    for (int kk = kKeys / 32; kk < kKeys / 16; ++kk)
-                        mma_bf16_ts(tO, tS + kk * 8, db + kk * (2048 >> 4), id_o, 1u);
                 } else {  // only the 16-key steps that hold keys (one at least)
                     const int steps = max((left + 15) / 16, 1);
 #pragma unroll 1
@@ -642,7 +635,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const int nx = x ? w.n1 : w.n0;
                     if (!kv_wait()) break;
                     tc_fence_after();
-                    if (nx > 0) qk();
+                    if (nx > 0) qk(false);
                     kv_done(nx > 0);
                     if (nx == 0) mbar_arrive(&bars.q_empty);
                     if (nx == 1) mma_commit(&bars.q_empty);
@@ -658,8 +651,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         if (!ok) break;
                         kv_done(j < nx);
                         if (more) {
-                            if (j + 1 < nx) qk();
-                            pass_turn();
+                            if (j + 1 < nx)
+                                qk(true);
+                            else
+                                pass_turn();
                             kv_done(j + 1 < nx);
                             if (j + 2 == nx) mma_commit(&bars.q_empty);
                         } else {
@@ -679,7 +674,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         const bool mine = (j & 1) == x;
                         if (!kv_wait()) break;
                         tc_fence_after();
-                        if (mine) qk();
+                        if (mine) qk(false);
                         kv_done(mine);
                         if (mine && j + 2 >= w.n) mma_commit(&bars.q_empty);
                         if (!kv_wait()) break;
@@ -810,12 +805,6 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             pk[e] = pa_pack<T>(p.x, p.y);
                         }
                         tmem_st16(tS + q * 16, pk);
-                        if (q == 1) {  // half of the keys: the product may start
-                            tmem_st_wait();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars.p_half[x]);
-                        }
                     }
                     const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
                     l += t.x + t.y;
@@ -823,10 +812,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    if (!warp_live) mbar_arrive(&bars.p_half[x]);
-                    mbar_arrive(&bars.p_full[x]);
-                }
+                if (lane == 0) mbar_arrive(&bars.p_full[x]);
             }
             if (!ok) break;
             g += 2 * w.n;
