@@ -26,10 +26,14 @@
 // Per key tile and tile: S = Q K^T into tensor memory (fp32), the row's 128
 // scores into registers, the running maximum, p = 2^(scale log2e (s - m)) in
 // fp32, summed in fp32 and rounded to the 16-bit type over the scores, where
-// the product P V reads its A operand. p <= 2^8 and is at most half a step off
-// (2^-9 for bf16, 2^-12 for fp16 of itself), the precision that the values
-// have. The reference maximum moves only when a row's maximum passes it by
-// more than 2^8; the row's O is rescaled then. O stays in tensor memory.
+// the product P V reads its A operand, at most half a step off (2^-8 for bf16,
+// 2^-11 for fp16 of itself), the precision that the values have. The reference
+// m is a row's maximum over earlier key tiles: a tile's own maximum is formed
+// beside its exponentials, not before them (it took 300 of 1150 cycles between
+// S and P), and moves the reference for the next tile if it passes it by more
+// than 2^8, O being rescaled then. Only where it passes it by so much that p
+// might leave the type's range (2^15 for fp16; 2^60 for bf16) the tile is done
+// again with its own maximum. O stays in tensor memory.
 //
 // Tensor memory (512 columns): S of the tiles at 0 and 128 (P over S), O at
 // 256 and 256 + D.
@@ -55,6 +59,9 @@ enum { kWhole = 0, kShared = 1, kAlternate = 2 };
 constexpr int kWorkSlots = 3;
 constexpr int kKeys = 128;  // keys per tile
 constexpr float kPaRescaleLog2 = 8.f;
+// p = 2^x must stay finite in the type, its sums and products in fp32
+template <typename T>
+constexpr float kPaRedoLog2 = std::is_same<T, __half>::value ? 15.f : 60.f;
 constexpr int kSlab = 128 * 128;  // 128 rows x 64 16-bit channels
 
 template <int D>
@@ -141,6 +148,41 @@ template <>
 __device__ __forceinline__ uint32_t pa_pack<__half>(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// One lane of a converged warp, always the same. Products issued under it keep
+// their descriptors in uniform registers; issued by a lane of its own branch they
+// take several times the instructions, and the softmax warps beside them leave
+// few slots for those: 1660 instead of 1100 cycles for the 16 products of a key
+// tile (1024 at full rate), measured with two softmax warps per scheduler.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
+// The products with descriptors as (low, high) words: only the low one, which
+// holds the address, changes.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Instruction descriptor: fp32 D, A and B both bf16 or both fp16.
@@ -391,7 +433,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __shared__ uint32_t tmem_base_s;
     __shared__ volatile int abort_flag;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same in all lanes
     const WaitCtl wc{P.status, kDefaultWaitNs};
     const WaitCtl drain{P.status, kDefaultWaitNs};
     uint8_t *sQ = pa_smem, *sKV = pa_smem + 2 * G::TILE;
@@ -462,21 +505,15 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
 
-    // The next entry of the schedule; every role walks the same list (a whole
-    // warp, or for the products its first lane).
-    const bool one_lane = warp == kWarpMma || warp == kWarpMma + 1;
+    // The next entry of the schedule; every role walks the same list.
     int wn = 0;
-    const auto next_work = [&](PaWork &w) -> bool {
+    const auto next_work = [&](PaWork &w) -> bool {  // by the whole warp
         const int s = wn % kWorkSlots, use = wn / kWorkSlots;
         ++wn;
-        const bool ok = mbar_wait(&bars.w_full[s], use & 1, wc, kStatusTimeoutSync, &abort_flag, false);
-        if (one_lane) {
-            if (!ok) return false;
-        } else if (!__all_sync(~0u, ok)) {
+        if (!__all_sync(~0u, mbar_wait(&bars.w_full[s], use & 1, wc, kStatusTimeoutSync, &abort_flag, false)))
             return false;
-        }
         w = work[s];
-        if (!one_lane) __syncwarp();
+        __syncwarp();
         if (lane == 0) mbar_arrive(&bars.w_empty[s]);
         return w.head >= 0;
     };
@@ -539,47 +576,50 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
             __syncwarp();
-        } else if (lane == 0) {
+        } else {
             // -------------------------------------------- products of tile x
+            // The whole warp walks; one lane issues.
             const int x = warp - kWarpMma;
-            const uint64_t k_major = smem_desc(0, 16, 1024, kSwizzle128B);
-            const uint64_t mn_major = smem_desc(0, kSlab, 1024, kSwizzle128B);
-            const uint32_t aQ = (smem_u32(sQ) + (ALT ? 0 : x) * G::TILE) >> 4, aKV = smem_u32(sKV) >> 4;
-            const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * D;
+            const uint32_t hi = static_cast<uint32_t>(smem_desc(0, 0, 1024, kSwizzle128B) >> 32);
+            constexpr uint32_t kLboK = (16u >> 4) << 16, kLboV = static_cast<uint32_t>(kSlab >> 4) << 16;
+            const uint32_t aQ = ((smem_u32(sQ) + (ALT ? 0 : x) * G::TILE) >> 4) | kLboK;
+            const uint32_t aKV = smem_u32(sKV) >> 4;
+            const uint32_t tS = __shfl_sync(~0u, tmem, 0) + x * 128, tO = tS - x * 128 + 256 + x * D;
             const int q_steps = (P.d + 15) / 16;
             const uint32_t id_s = pa_idesc<T>(kKeys, false), id_o = pa_idesc<T>(q_steps * 16, true);
             int st = 0, ph = 0;  // stage and parity of the next K or V tile
             int it = 0, np = 0, no = 0;  // items, P tiles, outputs of this tile
             int turns = 0;
             bool ok = true;
-            PaWork w{};
 
-            const auto kv_wait = [&]() {
-                ok = ok && mbar_wait(&bars.kv_full[st], ph, wc, kStatusTimeoutLoad, &abort_flag, false);
+            const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code) {
+                ok = ok && __all_sync(~0u, mbar_wait(bar, parity, wc, code, &abort_flag, false));
                 return ok;
             };
+            const auto kv_wait = [&]() { return wait(&bars.kv_full[st], ph, kStatusTimeoutLoad); };
             // the stage after this one, which is waited for again later
             const auto kv_peek = [&]() {
                 const int s2 = st + 1 == G::STAGES ? 0 : st + 1;
-                ok = ok && mbar_wait(&bars.kv_full[s2], s2 == 0 ? ph ^ 1 : ph, wc, kStatusTimeoutLoad,
-                                     &abort_flag, false);
+                wait(&bars.kv_full[s2], s2 == 0 ? ph ^ 1 : ph, kStatusTimeoutLoad);
             };
-            // The two threads issue their P V and Q K^T in turn, so that the tiles
+            // The two warps issue their P V and Q K^T in turn, so that the tiles
             // stay half a period apart: without it they fall into step, both
             // softmaxes beside an idle tensor pipe and then both products.
             const auto take_turn = [&]() {
-                ok = ok && mbar_wait(&bars.turn[x], (turns & 1) ^ (x ^ 1), wc, kStatusTimeoutSync,
-                                     &abort_flag, false);
+                wait(&bars.turn[x], (turns & 1) ^ (x ^ 1), kStatusTimeoutSync);
                 ++turns;
-                return ok;
             };
-            const auto pass_turn = [&]() { mbar_arrive(&bars.turn[x ^ 1]); };
+            const auto pass_turn = [&]() {
+                if (elect_one()) mbar_arrive(&bars.turn[x ^ 1]);
+            };
             // done with the stage: after the products issued so far, or at once
             const auto kv_done = [&](bool used) {
-                if (used)
-                    mma_commit(&bars.kv_empty[st]);
-                else
-                    mbar_arrive(&bars.kv_empty[st]);
+                if (elect_one()) {
+                    if (used)
+                        mma_commit(&bars.kv_empty[st]);
+                    else
+                        mbar_arrive(&bars.kv_empty[st]);
+                }
                 if (++st == G::STAGES) {
                     st = 0;
                     ph ^= 1;
@@ -587,67 +627,79 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             // S = Q K^T; pass: hand the turn over while the last products are issued
             const auto qk = [&](bool pass) {
-                const uint64_t da = k_major | aQ, db = k_major | (aKV + st * (G::TILE >> 4));
+                const uint32_t b = (aKV + st * (G::TILE >> 4)) | kLboK;
                 if (q_steps == D / 16) {
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
-                        mma_bf16_ss(tS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
-                        if (kk == D / 16 - 3 && pass) pass_turn();
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
+                            mma_ss(tS, aQ + off, b + off, hi, id_s, kk > 0 ? 1u : 0u);
+                            if (kk == D / 16 - 3 && pass) mbar_arrive(&bars.turn[x ^ 1]);
+                        }
+                        mma_commit(&bars.s_full[x]);
                     }
-                } else {  // channels past d are zero in shared memory: left out
+                } else if (elect_one()) {  // channels past d are zero in shared memory: left out
 #pragma unroll 1
                     for (int kk = 0; kk < q_steps; ++kk) {
                         const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
-                        mma_bf16_ss(tS, da + off, db + off, id_s, kk > 0 ? 1u : 0u);
+                        mma_ss(tS, aQ + off, b + off, hi, id_s, kk > 0 ? 1u : 0u);
                     }
-                    if (pass) pass_turn();
+                    if (pass) mbar_arrive(&bars.turn[x ^ 1]);
+                    mma_commit(&bars.s_full[x]);
                 }
-                mma_commit(&bars.s_full[x]);
             };
-            const auto pv = [&](int kt, bool first) {  // O (+)= P V
-                const int left = w.nk - kt * kKeys;
-                const uint64_t db = mn_major | (aKV + st * (G::TILE >> 4));
+            const auto pv = [&](int left, bool first) {  // O (+)= P V; left: keys of the tile
+                const uint32_t b = (aKV + st * (G::TILE >> 4)) | kLboV;
                 const uint32_t acc = first ? 0u : 1u;
-                ok = mbar_wait(&bars.p_full[x], np & 1, wc, kStatusTimeoutSync, &abort_flag, false);
+                if (!ALT) take_turn();
+                if (first) wait(&bars.o_empty[x], (no & 1) ^ 1, kStatusTimeoutSync);
+                if (!wait(&bars.p_full[x], np & 1, kStatusTimeoutSync)) return;
                 ++np;
-                if (ok && first)
-                    ok = mbar_wait(&bars.o_empty[x], (no & 1) ^ 1, wc, kStatusTimeoutSync, &abort_flag, false);
-                if (!ok || (!ALT && !take_turn())) return;
                 tc_fence_after();
                 if (left >= kKeys) {
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_bf16_ts(tO, tS + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
-                } else {  // only the 16-key steps that hold keys (one at least)
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            mma_ts(tO, tS + kk * 8, b + kk * (2048 >> 4), hi, id_o, kk > 0 ? 1u : acc);
+                    }
+                } else if (elect_one()) {  // only the 16-key steps that hold keys (one at least)
                     const int steps = max((left + 15) / 16, 1);
 #pragma unroll 1
                     for (int kk = 0; kk < steps; ++kk)
-                        mma_bf16_ts(tO, tS + kk * 8, db + kk * (2048 >> 4), id_o, kk > 0 ? 1u : acc);
+                        mma_ts(tO, tS + kk * 8, b + kk * (2048 >> 4), hi, id_o, kk > 0 ? 1u : acc);
                 }
             };
+            const auto q_done = [&]() {
+                if (elect_one()) mma_commit(&bars.q_empty);
+            };
+            const auto o_done = [&]() {
+                if (elect_one()) mma_commit(&bars.o_full[x]);
+                ++no;
+            };
 
+            PaWork w;
             while (ok && next_work(w)) {
-                ok = mbar_wait(&bars.q_full, it & 1, wc, kStatusTimeoutLoad, &abort_flag, false);
+                if (!wait(&bars.q_full, it & 1, kStatusTimeoutLoad)) break;
                 ++it;
+                const int n = __shfl_sync(~0u, w.n, 0);
+                const int nx = ALT ? (n + 1 - x) / 2 : __shfl_sync(~0u, x ? w.n1 : w.n0, 0);
+                const int keys = __shfl_sync(~0u, w.nk - w.lo * kKeys, 0);
+                if (nx == 0 && elect_one()) mbar_arrive(&bars.q_empty);
                 if constexpr (!ALT) {
                     // S(0); then per key tile: P V, S of the next
-                    const int nx = x ? w.n1 : w.n0;
                     if (!kv_wait()) break;
                     tc_fence_after();
                     if (nx > 0) qk(false);
                     kv_done(nx > 0);
-                    if (nx == 0) mbar_arrive(&bars.q_empty);
-                    if (nx == 1) mma_commit(&bars.q_empty);
-                    for (int j = 0; j < w.n; ++j) {
-                        const bool more = j + 1 < w.n;
+                    if (nx == 1) q_done();
+                    for (int j = 0; j < n; ++j) {
+                        const bool more = j + 1 < n;
                         if (!kv_wait()) break;
                         if (more) kv_peek();
-                        if (j < nx) {
-                            pv(w.lo + j, j == 0);
-                        } else {
+                        if (j < nx)
+                            pv(keys - j * kKeys, j == 0);
+                        else
                             take_turn();
-                        }
                         if (!ok) break;
                         kv_done(j < nx);
                         if (more) {
@@ -656,41 +708,36 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             else
                                 pass_turn();
                             kv_done(j + 1 < nx);
-                            if (j + 2 == nx) mma_commit(&bars.q_empty);
+                            if (j + 2 == nx) q_done();
                         } else {
                             pass_turn();
                         }
-                        if (j + 1 == nx) {
-                            mma_commit(&bars.o_full[x]);
-                            ++no;
-                        }
+                        if (j + 1 == nx) o_done();
                     }
                 } else {
-                    // this thread's key tiles are x, x + 2, ...; it lets go of the
+                    // this warp's key tiles are x, x + 2, ...; it lets go of the
                     // others as they land
-                    const int nx = (w.n + 1 - x) / 2;
-                    if (nx == 0) mbar_arrive(&bars.q_empty);
-                    for (int j = 0; j < w.n; ++j) {
+                    for (int j = 0; j < n; ++j) {
                         const bool mine = (j & 1) == x;
                         if (!kv_wait()) break;
                         tc_fence_after();
                         if (mine) qk(false);
                         kv_done(mine);
-                        if (mine && j + 2 >= w.n) mma_commit(&bars.q_empty);
+                        if (mine && j + 2 >= n) q_done();
                         if (!kv_wait()) break;
-                        if (mine) pv(w.lo + j, j < 2);
+                        if (mine) pv(keys - j * kKeys, j < 2);
                         if (!ok) break;
                         kv_done(mine);
-                        if (mine && j + 2 >= w.n) {
-                            mma_commit(&bars.o_full[x]);
-                            ++no;
-                        }
+                        if (mine && j + 2 >= n) o_done();
                     }
                 }
             }
             // drain: a last commit completes after every product issued here
-            mma_commit(&bars.fin[x]);
-            mbar_wait(&bars.fin[x], 0, drain, kStatusTimeoutDrain, nullptr);
+            __syncwarp();
+            if (elect_one()) {
+                mma_commit(&bars.fin[x]);
+                mbar_wait(&bars.fin[x], 0, drain, kStatusTimeoutDrain, nullptr);
+            }
         }
         __syncwarp();
     } else {
@@ -715,7 +762,9 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // masking is tested per warp against its first row, which sees least
             const int lim_first = P.causal ? min(w.nk, w.lim0 + shift_tok + tok_first) : w.nk;
             const bool warp_live = tok_first < toks && tok_first < P.tile_tokens;
-            float m = -INFINITY, l = 0.f;
+            // the reference, the one that the next tile takes, the sum (rows that
+            // do not exist keep a reference that asks for nothing)
+            float m = valid ? -INFINITY : 0.f, m_next = m, l = 0.f;
             for (int i = 0; i < n; ++i, ++ns) {
                 const int j = ALT ? 2 * i + x : i, kt = w.lo + j;
                 ok = __all_sync(~0u, mbar_wait(&bars.s_full[x], ns & 1, wc, kStatusTimeoutMma, &abort_flag,
@@ -754,60 +803,67 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             for (int e = 0; e < 32; ++e)
                                 if (q * 32 + e >= seen) s[q][e] = 0xFF800000u;  // -inf
                     }
-                    float mx = -INFINITY;
+                    if (__any_sync(~0u, m == -INFINITY)) {  // no reference yet
+                        float mx = -INFINITY;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float t[11];
+                        for (int q = 0; q < 4; ++q)
 #pragma unroll
-                        for (int e = 0; e < 10; ++e)
-                            t[e] = fmax3(__uint_as_float(s[q][3 * e]), __uint_as_float(s[q][3 * e + 1]),
-                                         __uint_as_float(s[q][3 * e + 2]));
-                        t[10] = fmaxf(__uint_as_float(s[q][30]), __uint_as_float(s[q][31]));
-                        const float a = fmax3(t[0], t[1], t[2]), b = fmax3(t[3], t[4], t[5]);
-                        const float d = fmax3(t[6], t[7], t[8]);
-                        mx = fmax3(mx, fmax3(a, b, d), fmaxf(t[9], t[10]));
+                            for (int e = 0; e < 32; e += 2)
+                                mx = fmax3(mx, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                        if (m == -INFINITY) m_next = mx * c;
                     }
-                    mx *= c;
-                    const bool grow = mx > m + kPaRescaleLog2 || (m == -INFINITY && mx > m);
-                    if (__any_sync(~0u, grow)) {
-                        const float alpha = grow ? (m == -INFINITY ? 0.f : ex2_approx(m - mx)) : 1.f;
-                        if (grow) m = mx;
-                        l *= alpha;
-                        if (i > 0) {
-                            // every earlier product of this tile is complete: the commit
-                            // behind these scores covers it
+                    float mx;
+                    while (true) {
+                        if (__any_sync(~0u, m_next > m)) {
+                            const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_next);
+                            m = m_next;
+                            l *= alpha;
+                            if (i > 0) {
+                                // every earlier product of this tile is complete: the
+                                // commit behind these scores covers it
 #pragma unroll 1
-                            for (int r = 0; r < D / 16; ++r) {
-                                uint32_t o[16];
-                                tmem_ld16(tO + r * 16, o);
-                                tmem_ld_wait(o);
+                                for (int r = 0; r < D / 16; ++r) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tO + r * 16, o);
+                                    tmem_ld_wait(o);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                tmem_st16(tO + r * 16, o);
+                                    for (int e = 0; e < 16; ++e)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tmem_st16(tO + r * 16, o);
+                                }
                             }
                         }
-                    }
-                    const float mm = m == -INFINITY ? 0.f : m;
-                    const float2 nm = make_float2(-mm, -mm);
-                    float2 sum[4];
+                        const float mm = m == -INFINITY ? 0.f : m;
+                        const float2 nm = make_float2(-mm, -mm);
+                        float2 sum[4];
+                        float top[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t pk[16];
-                        sum[q] = make_float2(0.f, 0.f);
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t pk[16];
+                            sum[q] = make_float2(0.f, 0.f);
+                            top[q] = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 y = ffma2(make_float2(__uint_as_float(s[q][2 * e]),
-                                                               __uint_as_float(s[q][2 * e + 1])),
-                                                   c2, nm);
-                            const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                            sum[q] = fadd2(sum[q], p);
-                            pk[e] = pa_pack<T>(p.x, p.y);
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 v = make_float2(__uint_as_float(s[q][2 * e]),
+                                                             __uint_as_float(s[q][2 * e + 1]));
+                                const float2 y = ffma2(v, c2, nm);
+                                const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                                sum[q] = fadd2(sum[q], p);
+                                top[q] = fmax3(top[q], v.x, v.y);
+                                pk[e] = pa_pack<T>(p.x, p.y);
+                            }
+                            tmem_st16(tS + q * 16, pk);
                         }
-                        tmem_st16(tS + q * 16, pk);
+                        mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+                        const bool redo = valid && mx > mm + kPaRedoLog2<T>;
+                        if (!__any_sync(~0u, redo)) {
+                            const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                            l += t.x + t.y;
+                            break;
+                        }
+                        if (redo) m_next = mx;
                     }
-                    const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
-                    l += t.x + t.y;
+                    if (valid && mx > m + kPaRescaleLog2) m_next = mx;
                     tmem_st_wait();
                     tc_fence_before();
                 }
