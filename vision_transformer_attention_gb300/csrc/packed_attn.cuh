@@ -28,11 +28,11 @@
 // fp32, summed in fp32 and rounded to the 16-bit type over the scores, where
 // the product P V reads its A operand, at most half a step off (2^-8 for bf16,
 // 2^-11 for fp16 of itself), the precision that the values have. The reference
-// m is a row's maximum over earlier key tiles: a tile's own maximum is formed
-// beside its exponentials, not before them (it took 300 of 1150 cycles between
-// S and P), and moves the reference for the next tile if it passes it by more
-// than 2^8, O being rescaled then. Only where it passes it by so much that p
-// might leave the type's range (2^15 for fp16; 2^60 for bf16) the tile is done
+// m is the row's maximum over its first key tile; later tiles form no maximum
+// (it took 300 of the 1150 cycles between S and P): a tile whose sum passes 2^8
+// moves the reference by log2 of it, which is within 2^7 of its maximum, for
+// the next tile, O being rescaled then; only where the sum says that a p may
+// have left the type's range (2^15 for fp16; 2^60 for bf16) the tile is done
 // again with its own maximum. O stays in tensor memory.
 //
 // Tensor memory (512 columns): S of the tiles at 0 and 128 (P over S), O at
@@ -58,10 +58,11 @@ constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 11;  // kWarpMma + tile
 enum { kWhole = 0, kShared = 1, kAlternate = 2 };
 constexpr int kWorkSlots = 3;
 constexpr int kKeys = 128;  // keys per tile
-constexpr float kPaRescaleLog2 = 8.f;
-// p = 2^x must stay finite in the type, its sums and products in fp32
+constexpr float kPaMove = 256.f;  // a tile's sum that moves the reference
+// ... and one that has the tile done again: every p is below its tile's sum, so
+// p stays finite in the type, and its products and sums in fp32
 template <typename T>
-constexpr float kPaRedoLog2 = std::is_same<T, __half>::value ? 15.f : 60.f;
+constexpr float kPaRedo = std::is_same<T, __half>::value ? 0x1p15f : 0x1p60f;
 constexpr int kSlab = 128 * 128;  // 128 rows x 64 16-bit channels
 
 template <int D>
@@ -634,7 +635,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
                             mma_ss(tS, aQ + off, b + off, hi, id_s, kk > 0 ? 1u : 0u);
-                            if (kk == D / 16 - 3 && pass) mbar_arrive(&bars.turn[x ^ 1]);
+                            if (kk == D / 16 - 2 && pass) mbar_arrive(&bars.turn[x ^ 1]);
                         }
                         mma_commit(&bars.s_full[x]);
                     }
@@ -803,19 +804,21 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             for (int e = 0; e < 32; ++e)
                                 if (q * 32 + e >= seen) s[q][e] = 0xFF800000u;  // -inf
                     }
-                    if (__any_sync(~0u, m == -INFINITY)) {  // no reference yet
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                mx = fmax3(mx, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-                        if (m == -INFINITY) m_next = mx * c;
-                    }
-                    float mx;
+                    bool own = m == -INFINITY;  // no reference yet: the tile's maximum
+                    float part;
                     while (true) {
-                        if (__any_sync(~0u, m_next > m)) {
-                            const float alpha = m == -INFINITY ? 0.f : ex2_approx(m - m_next);
+                        if (__any_sync(~0u, own || m_next > m)) {
+                            if (__any_sync(~0u, own)) {
+                                float mx = -INFINITY;
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2)
+                                        mx = fmax3(mx, __uint_as_float(s[q][e]),
+                                                   __uint_as_float(s[q][e + 1]));
+                                if (own) m_next = fmaxf(m, mx * c);
+                            }
+                            const float alpha = m_next > m ? (m == -INFINITY ? 0.f : ex2_approx(m - m_next)) : 1.f;
                             m = m_next;
                             l *= alpha;
                             if (i > 0) {
@@ -836,34 +839,28 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         const float mm = m == -INFINITY ? 0.f : m;
                         const float2 nm = make_float2(-mm, -mm);
                         float2 sum[4];
-                        float top[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t pk[16];
                             sum[q] = make_float2(0.f, 0.f);
-                            top[q] = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                const float2 v = make_float2(__uint_as_float(s[q][2 * e]),
-                                                             __uint_as_float(s[q][2 * e + 1]));
-                                const float2 y = ffma2(v, c2, nm);
+                                const float2 y = ffma2(make_float2(__uint_as_float(s[q][2 * e]),
+                                                                   __uint_as_float(s[q][2 * e + 1])),
+                                                       c2, nm);
                                 const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
                                 sum[q] = fadd2(sum[q], p);
-                                top[q] = fmax3(top[q], v.x, v.y);
                                 pk[e] = pa_pack<T>(p.x, p.y);
                             }
                             tmem_st16(tS + q * 16, pk);
                         }
-                        mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-                        const bool redo = valid && mx > mm + kPaRedoLog2<T>;
-                        if (!__any_sync(~0u, redo)) {
-                            const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
-                            l += t.x + t.y;
-                            break;
-                        }
-                        if (redo) m_next = mx;
+                        const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                        part = t.x + t.y;
+                        own = valid && part > kPaRedo<T>;
+                        if (!__any_sync(~0u, own)) break;
                     }
-                    if (valid && mx > m + kPaRescaleLog2) m_next = mx;
+                    l += part;
+                    if (valid && part > kPaMove) m_next = m + __log2f(part);
                     tmem_st_wait();
                     tc_fence_before();
                 }
