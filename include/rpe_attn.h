@@ -450,8 +450,8 @@ enum { RPE_ATTN_CAUSAL = 1 };
  * lse -infinity. Rows of out and lse that belong to no sequence stay as they
  * were. Scores of unseen keys do not matter, NaN included, nor do k and v
  * behind a sequence's keys; but a v row of the sequence that is infinite or
- * NaN reaches every query that sees a key of the same 128-key tile of the
- * sequence.
+ * NaN reaches every query that sees a key of the same tile of the sequence's
+ * keys (128 of them, 96 for d <= 64, from the first on).
  * Scores, maxima, sums and the output accumulate in fp32; the probabilities
  * are rounded to the 16-bit type before the value product. Results do not
  * depend on timing (no atomics).

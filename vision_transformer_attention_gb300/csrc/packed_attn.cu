@@ -154,10 +154,10 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     // without any key the maps read q's first row instead (every score is masked)
     const rpe_view none{q->data, 0, 0, 0};
     const int64_t rows_k = total_k > 0 ? total_k : 1;
-    const int heads_m = total_k > 0 ? heads_kv : 1;
+    const int heads_m = total_k > 0 ? heads_kv : 1, keys = d <= 64 ? 96 : 128;  // of a key tile
     if (!token_map(&m.q, dtype, *q, total_q, heads_q, d, a.group, p.tile_tokens) ||
-        !token_map(&m.k, dtype, total_k > 0 ? *k : none, rows_k, heads_m, d, 1, 128) ||
-        !token_map(&m.v, dtype, total_k > 0 ? *v : none, rows_k, heads_m, d, 1, 128))
+        !token_map(&m.k, dtype, total_k > 0 ? *k : none, rows_k, heads_m, d, 1, keys) ||
+        !token_map(&m.v, dtype, total_k > 0 ? *v : none, rows_k, heads_m, d, 1, keys))
         return RPE_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!status_word_ready(st)) return RPE_ERR_UNSUPPORTED;

@@ -7,7 +7,7 @@
 //
 // Tiles. The g query heads that share a key/value head sit side by side in
 // memory, so a tile of 128 rows holds TQ = 128 / g tokens x g heads (one TMA
-// box), and every key tile (128 keys) is read once for all of them. A CTA works
+// box), and every key tile is read once for all of them. A CTA works
 // on two such tiles at a time, each with its own softmax warpgroup, one thread
 // per row, and its own issuing thread for the tensor-core products, so that one
 // tile's softmax and waits run under the other's products (with one issuing
@@ -23,7 +23,7 @@
 // unnormalised outputs go to the caller's workspace in fp32, and
 // packed_combine_kernel joins them.
 //
-// Per key tile and tile: S = Q K^T into tensor memory (fp32), the row's 128
+// Per key tile (128 keys, or 96 for D = 64) and tile: S = Q K^T into tensor memory (fp32), the row's 128
 // scores into registers, the running maximum, p = 2^(scale log2e (s - m)) in
 // fp32, summed in fp32 and rounded to the 16-bit type over the scores, where
 // the product P V reads its A operand, at most half a step off (2^-8 for bf16,
@@ -35,8 +35,11 @@
 // have left the type's range (2^15 for fp16; 2^60 for bf16) the tile is done
 // again with its own maximum. O stays in tensor memory.
 //
-// Tensor memory (512 columns): S of the tiles at 0 and 128 (P over S), O at
-// 256 and 256 + D.
+// Tensor memory (512 columns). D = 128: S of the tiles at 0 and 128 (P over S),
+// O at 256 and 384; the next S waits for P V. D = 64: O at 0 and 64 and two
+// slots of S per tile, for which key tiles have 96 keys: S of the tile after
+// next is formed behind P V, and a softmax finds its S ready. (128 keys in one
+// slot with P beside it took 2400 cycles per 128 keys and pair of tiles.)
 //
 // Keys past a sequence's end and, in the tile on the diagonal, past a row's
 // last key are masked in registers whatever their scores are; V rows past the
@@ -57,7 +60,6 @@ static_assert(128 * kPaRegsControl + 256 * kPaRegsSoftmax <= kPaThreads * kPaReg
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 11;  // kWarpMma + tile
 enum { kWhole = 0, kShared = 1, kAlternate = 2 };
 constexpr int kWorkSlots = 3;
-constexpr int kKeys = 128;  // keys per tile
 constexpr float kPaMove = 256.f;  // a tile's sum that moves the reference
 // ... and one that has the tile done again: every p is below its tile's sum, so
 // p stays finite in the type, and its products and sums in fp32
@@ -67,10 +69,14 @@ constexpr int kSlab = 128 * 128;  // 128 rows x 64 16-bit channels
 
 template <int D>
 struct PaGeo {
+    static constexpr int KEYS = D == 64 ? 96 : 128;  // per key tile
     static constexpr int SLABS = D / 64;
-    static constexpr int TILE = SLABS * kSlab;  // one Q, K or V tile
-    static constexpr int STAGES = D == 128 ? 5 : 10;  // K and V tiles in flight
-    static constexpr int SMEM = (2 + STAGES) * TILE;
+    static constexpr int Q_TILE = SLABS * kSlab;
+    static constexpr int KV_SLAB = KEYS * 128, TILE = SLABS * KV_SLAB;  // one K or V tile
+    static constexpr int STAGES = D == 128 ? 5 : 15;  // K and V tiles in flight
+    static constexpr int SMEM = 2 * Q_TILE + STAGES * TILE;
+    static constexpr int SLOTS = D == 64 ? 2 : 1;  // S of a tile in tensor memory
+    static constexpr uint32_t O_COL = D == 64 ? 0 : 256, S_COL = D == 64 ? 128 : 0;
 };
 
 // One unit of work, as the schedule warp hands it to the others.
@@ -87,8 +93,9 @@ struct PaWork {
 
 struct PaBars {
     uint64_t q_full, q_empty;
-    uint64_t kv_full[10], kv_empty[10];
-    uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t kv_full[15], kv_empty[15];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // tile, slot
+    uint64_t o_empty[2];
     uint64_t w_full[kWorkSlots], w_empty[kWorkSlots];
     uint64_t turn[2], fin[2];
 };
@@ -116,9 +123,10 @@ __device__ __forceinline__ PaSeq pa_seq(const PackedAttnArgs &P, int b, bool *ba
 
 // Key tiles that the tokens up to `last` of a sequence need (at least one, so
 // that rows without keys are written too).
+template <int KEYS>
 __device__ __forceinline__ int pa_tiles(const PackedAttnArgs &P, const PaSeq &s, int last) {
     const int vis = P.causal ? min(s.nk, last + 1 + s.nk - s.nq) : s.nk;
-    return vis <= kKeys ? 1 : (vis + kKeys - 1) / kKeys;
+    return vis <= KEYS ? 1 : (vis + KEYS - 1) / KEYS;
 }
 
 __device__ __forceinline__ int warp_sum(int v) {
@@ -220,6 +228,7 @@ struct PaRing {
 
 // Whole items, the costliest first (by key tiles, in at most 64 levels), dealt
 // to the CTAs round by round, every other round backwards.
+template <int KEYS>
 __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRing ring, int lane,
                                                   int most_tiles) {
     const int TT = 2 * P.tile_tokens;
@@ -236,7 +245,7 @@ __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRin
     const auto upto = [&](const PaSeq &s, int q) -> int {
         if (q < 0) return 0;
         const int nb = (s.nq + TT - 1) / TT;
-        const long long keys = (static_cast<long long>(q + 1) << shift) * kKeys;
+        const long long keys = (static_cast<long long>(q + 1) << shift) * KEYS;
         if (s.nk <= keys) return nb;
         if (!P.causal) return 0;
         const long long t = (keys - (s.nk - s.nq)) / TT;
@@ -271,8 +280,8 @@ __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRin
                 w.nk = q_seq.nk;
                 w.lim0 = tok + 1 + q_seq.nk - q_seq.nq;
                 w.lo = 0;
-                w.n0 = pa_tiles(P, q_seq, min(q_seq.nq, tok + P.tile_tokens) - 1);
-                w.n1 = w.toks > P.tile_tokens ? pa_tiles(P, q_seq, min(q_seq.nq, tok + TT) - 1) : 0;
+                w.n0 = pa_tiles<KEYS>(P, q_seq, min(q_seq.nq, tok + P.tile_tokens) - 1);
+                w.n1 = w.toks > P.tile_tokens ? pa_tiles<KEYS>(P, q_seq, min(q_seq.nq, tok + TT) - 1) : 0;
                 w.n = max(w.n0, w.n1);
                 w.slot = 0;
                 alive = ring.put(w, lane);
@@ -291,20 +300,22 @@ __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRin
 
 // Units (key tiles of one item) and items of a sequence; an item is TT tokens
 // of one key/value head.
+template <int KEYS>
 __device__ __forceinline__ void pa_units(const PackedAttnArgs &P, const PaSeq &s, int TT,
                                          long long *units, int *items) {
     long long u = 0;
     const int nt = (s.nq + TT - 1) / TT;
     if (!P.causal || nt <= 1)
-        u = static_cast<long long>(nt) * (nt ? pa_tiles(P, s, s.nq - 1) : 0);
+        u = static_cast<long long>(nt) * (nt ? pa_tiles<KEYS>(P, s, s.nq - 1) : 0);
     else
-        for (int t = 0; t < nt; ++t) u += pa_tiles(P, s, min(s.nq, (t + 1) * TT) - 1);
+        for (int t = 0; t < nt; ++t) u += pa_tiles<KEYS>(P, s, min(s.nq, (t + 1) * TT) - 1);
     *units = u * P.heads_kv;
     *items = nt * P.heads_kv;
 }
 
 // Shared and alternate: this CTA's share [u0, u1) of all units, in (sequence,
 // tokens, head, key tile) order. per: sequences per warp of the count before.
+template <int KEYS>
 __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRing ring, int lane,
                                                    int TT, const long long *warp_units,
                                                    const int *warp_tiles, int per) {
@@ -348,7 +359,7 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
             s = PaSeq{0, 0, 0, 0};
             if (b + lane < P.batch) {
                 s = pa_seq(P, b + lane, &bad);
-                pa_units(P, s, TT, &u, &n);
+                pa_units<KEYS>(P, s, TT, &u, &n);
             }
             const long long us = warp_scan(u, lane);
             const int ns = warp_scan(n, lane);
@@ -374,7 +385,7 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
     int4 *meta = reinterpret_cast<int4 *>(header + 16);
     for (int t = 0; u < u1;) {
         const int last = min(s.nq, (t + 1) * TT) - 1;
-        const int kt = pa_tiles(P, s, last);
+        const int kt = pa_tiles<KEYS>(P, s, last);
         const long long span = static_cast<long long>(kt) * P.heads_kv;
         if (t * TT >= s.nq) {  // next sequence
             ++b;
@@ -403,7 +414,7 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
         w.lim0 = tok + 1 + s.nk - s.nq;
         w.lo = lo;
         w.n = n;
-        const int kt0 = pa_tiles(P, s, min(s.nq, tok + P.tile_tokens) - 1);
+        const int kt0 = pa_tiles<KEYS>(P, s, min(s.nq, tok + P.tile_tokens) - 1);
         w.n0 = min(max(kt0 - lo, 0), n);
         w.n1 = w.toks > P.tile_tokens ? n : 0;
         w.slot = item + h + blockIdx.x;
@@ -426,6 +437,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PackedAttnArgs P) {
     using G = PaGeo<D>;
     constexpr bool ALT = KIND == kAlternate, PIECES = KIND != kWhole;
+    constexpr int KEYS = G::KEYS, SLOTS = ALT ? 1 : G::SLOTS;
     extern __shared__ __align__(1024) uint8_t pa_smem[];
     __shared__ PaBars bars;
     __shared__ PaWork work[kWorkSlots];
@@ -438,7 +450,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same in all lanes
     const WaitCtl wc{P.status, kDefaultWaitNs};
     const WaitCtl drain{P.status, kDefaultWaitNs};
-    uint8_t *sQ = pa_smem, *sKV = pa_smem + 2 * G::TILE;
+    uint8_t *sQ = pa_smem, *sKV = pa_smem + 2 * G::Q_TILE;
 
     if (tid == 0) {
         mbar_init(&bars.q_full, 1);
@@ -448,9 +460,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_init(&bars.kv_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4);
-            mbar_init(&bars.o_full[i], 1);
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(&bars.s_full[i][s], 1);
+                mbar_init(&bars.p_full[i][s], 4);
+                mbar_init(&bars.pv_done[i][s], 1);
+            }
             mbar_init(&bars.o_empty[i], 4);
         }
         for (int i = 0; i < kWorkSlots; ++i) {
@@ -482,11 +496,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if constexpr (PIECES) {
                 long long u;
                 int n;
-                pa_units(P, s, TT, &u, &n);
+                pa_units<KEYS>(P, s, TT, &u, &n);
                 units += u;
                 tiles += n;
             } else {
-                tiles = max(tiles, pa_tiles(P, s, s.nq - 1));
+                tiles = max(tiles, pa_tiles<KEYS>(P, s, s.nq - 1));
             }
         }
         if (bad) atomicOr(P.status, kStatusBadSequence);
@@ -524,11 +538,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (warp == kWarpSched) {
             PaRing ring{work, bars.w_full, bars.w_empty, &wc, &abort_flag};
             if constexpr (PIECES) {
-                pa_schedule_pieces(P, ring, lane, TT, warp_units, warp_tiles, per);
+                pa_schedule_pieces<KEYS>(P, ring, lane, TT, warp_units, warp_tiles, per);
             } else {
                 int most = 1;
                 for (int i = 0; i < kPaThreads / 32; ++i) most = max(most, warp_tiles[i]);
-                pa_schedule_items(P, ring, lane, most);
+                pa_schedule_items<KEYS>(P, ring, lane, most);
             }
         } else if (warp == kWarpLoad) {
             if (lane == 0) {
@@ -549,11 +563,16 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mbar_arrive_expect_tx(&bars.q_full, tiles_q * q_bytes);
                     for (int i = 0; i < tiles_q; ++i)
                         for (int sl = 0; sl < G::SLABS; ++sl)
-                            tma_load_3d(sQ + i * G::TILE + sl * kSlab, &tm_q, &bars.q_full, sl * 64,
+                            tma_load_3d(sQ + i * G::Q_TILE + sl * kSlab, &tm_q, &bars.q_full, sl * 64,
                                         w.head * P.group, w.q_tok + i * P.tile_tokens);
                 }
-                for (int j = 0; j < 2 * w.n; ++j, ++g) {  // K0 V0 K1 V1 ...
-                    const bool is_k = (j & 1) == 0;
+                // in the order of use: K0 V0 K1 V1 ..., with two slots of S
+                // K0 K1 V0 K2 V1 ...
+                for (int j = 0; j < 2 * w.n; ++j, ++g) {
+                    const bool is_k = SLOTS == 1 ? (j & 1) == 0 : j == 0 || ((j & 1) != 0 && j < 2 * w.n - 1);
+                    const int kt = SLOTS == 1 ? j / 2
+                                   : is_k     ? (j + 1) / 2
+                                              : (j == 2 * w.n - 1 ? w.n - 1 : j / 2 - 1);
                     const int st = g % G::STAGES, use = g / G::STAGES;
                     ok = __all_sync(~0u, mbar_wait(&bars.kv_empty[st], (use & 1) ^ 1, wc,
                                                    kStatusTimeoutSync, &abort_flag, false));
@@ -561,9 +580,9 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bars.kv_full[st], G::TILE);
                         for (int sl = 0; sl < G::SLABS; ++sl)
-                            tma_load_3d(sKV + st * G::TILE + sl * kSlab, is_k ? &tm_k : &tm_v,
+                            tma_load_3d(sKV + st * G::TILE + sl * G::KV_SLAB, is_k ? &tm_k : &tm_v,
                                         &bars.kv_full[st], sl * 64, w.head,
-                                        w.k_row + (w.lo + j / 2) * kKeys);
+                                        w.k_row + (w.lo + kt) * KEYS);
                     }
                 }
             }
@@ -582,14 +601,16 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // The whole warp walks; one lane issues.
             const int x = warp - kWarpMma;
             const uint32_t hi = static_cast<uint32_t>(smem_desc(0, 0, 1024, kSwizzle128B) >> 32);
-            constexpr uint32_t kLboK = (16u >> 4) << 16, kLboV = static_cast<uint32_t>(kSlab >> 4) << 16;
-            const uint32_t aQ = ((smem_u32(sQ) + (ALT ? 0 : x) * G::TILE) >> 4) | kLboK;
+            constexpr uint32_t kLboK = (16u >> 4) << 16, kLboV = static_cast<uint32_t>(G::KV_SLAB >> 4) << 16;
+            const uint32_t aQ = ((smem_u32(sQ) + (ALT ? 0 : x) * G::Q_TILE) >> 4) | kLboK;
             const uint32_t aKV = smem_u32(sKV) >> 4;
-            const uint32_t tS = __shfl_sync(~0u, tmem, 0) + x * 128, tO = tS - x * 128 + 256 + x * D;
+            const uint32_t t0 = __shfl_sync(~0u, tmem, 0);
+            const uint32_t tS0 = t0 + G::S_COL + x * KEYS * G::SLOTS, tO = t0 + G::O_COL + x * D;
             const int q_steps = (P.d + 15) / 16;
-            const uint32_t id_s = pa_idesc<T>(kKeys, false), id_o = pa_idesc<T>(q_steps * 16, true);
+            const uint32_t id_s = pa_idesc<T>(KEYS, false), id_o = pa_idesc<T>(q_steps * 16, true);
             int st = 0, ph = 0;  // stage and parity of the next K or V tile
-            int it = 0, np = 0, no = 0;  // items, P tiles, outputs of this tile
+            int it = 0, ns = 0, np = 0, no = 0;  // items, S and P tiles, outputs of this tile
+            const auto slot = [&](int i) { return tS0 + (SLOTS == 2 && (i & 1) ? KEYS : 0); };
             int turns = 0;
             bool ok = true;
 
@@ -628,25 +649,29 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             // S = Q K^T; pass: hand the turn over while the last products are issued
             const auto qk = [&](bool pass) {
+                uint64_t *full = &bars.s_full[x][SLOTS == 2 ? ns & 1 : 0];
+                const uint32_t tS = slot(ns++);
                 const uint32_t b = (aKV + st * (G::TILE >> 4)) | kLboK;
                 if (q_steps == D / 16) {
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
-                            mma_ss(tS, aQ + off, b + off, hi, id_s, kk > 0 ? 1u : 0u);
+                            const uint32_t in = (kk & 3) * (32 >> 4), sl = kk >> 2;
+                            mma_ss(tS, aQ + sl * (kSlab >> 4) + in, b + sl * (G::KV_SLAB >> 4) + in, hi, id_s,
+                                   kk > 0 ? 1u : 0u);
                             if (kk == D / 16 - 2 && pass) mbar_arrive(&bars.turn[x ^ 1]);
                         }
-                        mma_commit(&bars.s_full[x]);
+                        mma_commit(full);
                     }
                 } else if (elect_one()) {  // channels past d are zero in shared memory: left out
 #pragma unroll 1
                     for (int kk = 0; kk < q_steps; ++kk) {
-                        const uint32_t off = (kk >> 2) * (kSlab >> 4) + (kk & 3) * (32 >> 4);
-                        mma_ss(tS, aQ + off, b + off, hi, id_s, kk > 0 ? 1u : 0u);
+                        const uint32_t in = (kk & 3) * (32 >> 4), sl = kk >> 2;
+                        mma_ss(tS, aQ + sl * (kSlab >> 4) + in, b + sl * (G::KV_SLAB >> 4) + in, hi, id_s,
+                               kk > 0 ? 1u : 0u);
                     }
                     if (pass) mbar_arrive(&bars.turn[x ^ 1]);
-                    mma_commit(&bars.s_full[x]);
+                    mma_commit(full);
                 }
             };
             const auto pv = [&](int left, bool first) {  // O (+)= P V; left: keys of the tile
@@ -654,66 +679,67 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const uint32_t acc = first ? 0u : 1u;
                 if (!ALT) take_turn();
                 if (first) wait(&bars.o_empty[x], (no & 1) ^ 1, kStatusTimeoutSync);
-                if (!wait(&bars.p_full[x], np & 1, kStatusTimeoutSync)) return;
-                ++np;
+                if (!wait(&bars.p_full[x][SLOTS == 2 ? np & 1 : 0], (SLOTS == 2 ? np >> 1 : np) & 1,
+                          kStatusTimeoutSync))
+                    return;
+                uint64_t *done = &bars.pv_done[x][SLOTS == 2 ? np & 1 : 0];
+                const uint32_t tP = slot(np++);
                 tc_fence_after();
-                if (left >= kKeys) {
+                if (left >= KEYS) {
                     if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_ts(tO, tS + kk * 8, b + kk * (2048 >> 4), hi, id_o, kk > 0 ? 1u : acc);
+                        for (int kk = 0; kk < KEYS / 16; ++kk)
+                            mma_ts(tO, tP + kk * 8, b + kk * (2048 >> 4), hi, id_o, kk > 0 ? 1u : acc);
+                        mma_commit(done);
                     }
-                } else if (elect_one()) {  // only the 16-key steps that hold keys (one at least)
+                } else {  // only the 16-key steps that hold keys (one at least)
                     const int steps = max((left + 15) / 16, 1);
+                    if (elect_one()) {
 #pragma unroll 1
-                    for (int kk = 0; kk < steps; ++kk)
-                        mma_ts(tO, tS + kk * 8, b + kk * (2048 >> 4), hi, id_o, kk > 0 ? 1u : acc);
+                        for (int kk = 0; kk < steps; ++kk)
+                            mma_ts(tO, tP + kk * 8, b + kk * (2048 >> 4), hi, id_o, kk > 0 ? 1u : acc);
+                        mma_commit(done);
+                    }
                 }
             };
             const auto q_done = [&]() {
                 if (elect_one()) mma_commit(&bars.q_empty);
             };
-            const auto o_done = [&]() {
-                if (elect_one()) mma_commit(&bars.o_full[x]);
-                ++no;
-            };
-
             PaWork w;
             while (ok && next_work(w)) {
                 if (!wait(&bars.q_full, it & 1, kStatusTimeoutLoad)) break;
                 ++it;
                 const int n = __shfl_sync(~0u, w.n, 0);
                 const int nx = ALT ? (n + 1 - x) / 2 : __shfl_sync(~0u, x ? w.n1 : w.n0, 0);
-                const int keys = __shfl_sync(~0u, w.nk - w.lo * kKeys, 0);
+                const int keys = __shfl_sync(~0u, w.nk - w.lo * KEYS, 0);
                 if (nx == 0 && elect_one()) mbar_arrive(&bars.q_empty);
                 if constexpr (!ALT) {
-                    // S(0); then per key tile: P V, S of the next
-                    if (!kv_wait()) break;
-                    tc_fence_after();
-                    if (nx > 0) qk(false);
-                    kv_done(nx > 0);
-                    if (nx == 1) q_done();
+                    // the first S; then per key tile: P V, and S in the slot it frees
+                    for (int j = 0; j < SLOTS && j < n; ++j) {
+                        if (!kv_wait()) break;
+                        tc_fence_after();
+                        if (j < nx) qk(false);
+                        kv_done(j < nx);
+                    }
+                    if (!ok) break;
+                    if (nx > 0 && nx <= SLOTS) q_done();
                     for (int j = 0; j < n; ++j) {
-                        const bool more = j + 1 < n;
+                        const bool more = j + SLOTS < n, mine = j + SLOTS < nx;
                         if (!kv_wait()) break;
                         if (more) kv_peek();
                         if (j < nx)
-                            pv(keys - j * kKeys, j == 0);
+                            pv(keys - j * KEYS, j == 0);
                         else
                             take_turn();
                         if (!ok) break;
                         kv_done(j < nx);
-                        if (more) {
-                            if (j + 1 < nx)
-                                qk(true);
-                            else
-                                pass_turn();
-                            kv_done(j + 1 < nx);
-                            if (j + 2 == nx) q_done();
-                        } else {
+                        if (mine)
+                            qk(true);
+                        else
                             pass_turn();
-                        }
-                        if (j + 1 == nx) o_done();
+                        if (more) kv_done(mine);
+                        if (j + SLOTS + 1 == nx) q_done();
+                        if (j + 1 == nx) ++no;
                     }
                 } else {
                     // this warp's key tiles are x, x + 2, ...; it lets go of the
@@ -726,10 +752,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         kv_done(mine);
                         if (mine && j + 2 >= n) q_done();
                         if (!kv_wait()) break;
-                        if (mine) pv(keys - j * kKeys, j < 2);
+                        if (mine) pv(keys - j * KEYS, j < 2);
                         if (!ok) break;
                         kv_done(mine);
-                        if (mine && j + 2 >= n) o_done();
+                        if (mine && j + 2 >= n) ++no;
                     }
                 }
             }
@@ -748,10 +774,19 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int tok = row / P.group, hd = row - tok * P.group;
         const int tok_first = (row & ~31) / P.group; // token of the warp's first row
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane field: 32 * warp
-        const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * D;
-        int ns = 0, no = 0, g = 0;  // S tiles and outputs of this tile, K and V tiles
+        const uint32_t tS0 = tmem + lanes + G::S_COL + x * KEYS * G::SLOTS, tO = tmem + lanes + G::O_COL + x * D;
+        int ns = 0, g = 0;  // S tiles of this tile, K and V tiles
         const float c = P.scale_log2;
         const float2 c2 = make_float2(c, c);
+        // The P V before S tile ns is complete. (Of the barrier of its slot, the
+        // P V two before it is complete, since S tile ns - 1 came behind it, and
+        // none after it can be: the phase is unambiguous.)
+        const auto pv_over = [&]() {
+            const int k = ns - 1;
+            return __all_sync(~0u, mbar_wait(&bars.pv_done[x][SLOTS == 2 ? k & 1 : 0],
+                                             (SLOTS == 2 ? k >> 1 : k) & 1, wc, kStatusTimeoutMma,
+                                             &abort_flag, false));
+        };
         PaWork w;
         bool ok = true;
         while (ok && next_work(w)) {
@@ -768,38 +803,43 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             float m = valid ? -INFINITY : 0.f, m_next = m, l = 0.f;
             for (int i = 0; i < n; ++i, ++ns) {
                 const int j = ALT ? 2 * i + x : i, kt = w.lo + j;
-                ok = __all_sync(~0u, mbar_wait(&bars.s_full[x], ns & 1, wc, kStatusTimeoutMma, &abort_flag,
-                                               false));
+                const int sl = SLOTS == 2 ? ns & 1 : 0;
+                ok = __all_sync(~0u, mbar_wait(&bars.s_full[x][sl], (SLOTS == 2 ? ns >> 1 : ns) & 1, wc,
+                                               kStatusTimeoutMma, &abort_flag, false));
                 if (!ok) break;
-                if (w.nk < (kt + 1) * kKeys) {
-                    // A part tile: V's rows behind the sequence in the last 16-key
-                    // step that the product reads become zero. (Of this stage's
-                    // fills the one before has been used, K behind it having given
-                    // S, and the one after waits for this P V, so the parity is
-                    // unambiguous. Both tiles may do this: they write the same.)
-                    const int idx = g + 2 * j + 1, st = idx % G::STAGES, use = idx / G::STAGES;
+                if (w.nk < (kt + 1) * KEYS) {
+                    // A part tile (the item's last): V's rows behind the sequence in
+                    // the last 16-key step that the product reads become zero. (Of
+                    // this stage's fills the one before has been used, K behind it
+                    // having given S, and the one after waits for this P V, so the
+                    // parity is unambiguous. Both tiles may do this: they write the
+                    // same.)
+                    const int idx = g + 2 * w.n - 1;
+                    const int st = idx % G::STAGES, use = idx / G::STAGES;
                     ok = __all_sync(~0u, mbar_wait(&bars.kv_full[st], use & 1, wc, kStatusTimeoutLoad,
                                                    &abort_flag, false));
                     if (!ok) break;
-                    const int keys = max(w.nk - kt * kKeys, 0), end = max((keys + 15) / 16, 1) * 16;
+                    const int keys = max(w.nk - kt * KEYS, 0), end = max((keys + 15) / 16, 1) * 16;
                     const uint32_t dst = smem_u32(sKV) + st * G::TILE;
-                    for (int sl = 0; sl < G::SLABS; ++sl)
+                    for (int k = 0; k < G::SLABS; ++k)
                         for (int e = keys * 8 + row; e < end * 8; e += 128)
-                            st_shared_v4(dst + sl * kSlab + e * 16, 0u, 0u, 0u, 0u);
+                            st_shared_v4(dst + k * G::KV_SLAB + e * 16, 0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
                 if (warp_live) {
                     tc_fence_after();
-                    uint32_t s[4][32];
+                    constexpr int NC = KEYS / 32;  // 32 scores at a time
+                    const uint32_t tS = tS0 + sl * KEYS;
+                    uint32_t s[NC][32];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, s[q]);
+                    for (int q = 0; q < NC; ++q) tmem_ld32(tS + q * 32, s[q]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ready(s[q]);
-                    const int seen = lim - kt * kKeys;  // columns that this row sees
-                    if (lim_first < (kt + 1) * kKeys) {
+                    for (int q = 0; q < NC; ++q) tmem_ready(s[q]);
+                    const int seen = lim - kt * KEYS;  // columns that this row sees
+                    if (lim_first < (kt + 1) * KEYS) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < NC; ++q)
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (q * 32 + e >= seen) s[q][e] = 0xFF800000u;  // -inf
@@ -811,7 +851,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             if (__any_sync(~0u, own)) {
                                 float mx = -INFINITY;
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
+                                for (int q = 0; q < NC; ++q)
 #pragma unroll
                                     for (int e = 0; e < 32; e += 2)
                                         mx = fmax3(mx, __uint_as_float(s[q][e]),
@@ -822,8 +862,14 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             m = m_next;
                             l *= alpha;
                             if (i > 0) {
-                                // every earlier product of this tile is complete: the
-                                // commit behind these scores covers it
+                                // once this tile's earlier products are complete (one
+                                // slot: they are, the commit behind these scores covers
+                                // them; two: all but the last)
+                                if (SLOTS == 2) {
+                                    ok = pv_over();
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                }
 #pragma unroll 1
                                 for (int r = 0; r < D / 16; ++r) {
                                     uint32_t o[16];
@@ -838,9 +884,9 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                         const float mm = m == -INFINITY ? 0.f : m;
                         const float2 nm = make_float2(-mm, -mm);
-                        float2 sum[4];
+                        float2 sum[NC];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < NC; ++q) {
                             uint32_t pk[16];
                             sum[q] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -854,26 +900,26 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             }
                             tmem_st16(tS + q * 16, pk);
                         }
-                        const float2 t = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                        float2 t = fadd2(fadd2(sum[0], sum[1]), sum[2]);
+                        if constexpr (NC == 4) t = fadd2(t, sum[3]);
                         part = t.x + t.y;
                         own = valid && part > kPaRedo<T>;
                         if (!__any_sync(~0u, own)) break;
                     }
+                    if (!ok) break;
                     l += part;
                     if (valid && part > kPaMove) m_next = m + __log2f(part);
                     tmem_st_wait();
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[x]);
+                if (lane == 0) mbar_arrive(&bars.p_full[x][sl]);
             }
             if (!ok) break;
             g += 2 * w.n;
             if (n > 0) {
-                ok = __all_sync(~0u, mbar_wait(&bars.o_full[x], no & 1, wc, kStatusTimeoutMma, &abort_flag,
-                                               false));
+                ok = pv_over();
                 if (!ok) break;
-                ++no;
                 tc_fence_after();
             }
             if constexpr (PIECES) {
