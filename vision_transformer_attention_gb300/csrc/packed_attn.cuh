@@ -92,7 +92,7 @@ struct PaWork {
 };
 
 struct PaBars {
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];  // alternate: only the first
     uint64_t kv_full[15], kv_empty[15];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // tile, slot
     uint64_t o_empty[2];
@@ -200,6 +200,39 @@ __device__ __forceinline__ uint32_t pa_idesc(int N, bool b_mn_major) {
     const uint32_t f = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     return (1u << 4) | (f << 7) | (f << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+
+// Writes 64 bytes of each of a warp's rows, held one row per thread in v. Four
+// neighbouring threads exchange their 16-byte units first, so that an
+// instruction writes 64 bytes of each of 8 rows and not 16 of each of 32 (which
+// took 62 cycles of the SM's store path each, 4000 for a tile of 128 x 128).
+// rows: the four threads' rows; at: the byte offset of the 64; bit i of rows_ok:
+// row i is to be written; unit_ok: this thread's unit (lane & 3) is.
+__device__ __forceinline__ void store_rows(uint32_t (&v)[16], char *const (&rows)[4], int at,
+                                           unsigned rows_ok, bool unit_ok, int lane) {
+    const int j = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {  // 4 x 4 transpose in two rounds
+        const int d = r == 0 ? 1 : 2;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int lo = r == 0 ? 2 * p : p, up = lo + d;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t a = v[4 * lo + k], b = v[4 * up + k];
+                const uint32_t got = __shfl_xor_sync(~0u, (j & d) ? a : b, d);
+                if (j & d)
+                    v[4 * lo + k] = got;
+                else
+                    v[4 * up + k] = got;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (unit_ok && ((rows_ok >> i) & 1u))
+            *reinterpret_cast<uint4 *>(rows[i] + at + 16 * j) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
 // ------------------------------------------------------------- schedule
@@ -453,8 +486,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint8_t *sQ = pa_smem, *sKV = pa_smem + 2 * G::Q_TILE;
 
     if (tid == 0) {
-        mbar_init(&bars.q_full, 1);
-        mbar_init(&bars.q_empty, 2);  // one arrival per issuing thread
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.q_full[i], 1);
+            mbar_init(&bars.q_empty[i], ALT ? 2 : 1);  // one arrival per warp that reads it
+        }
         for (int i = 0; i < G::STAGES; ++i) {
             mbar_init(&bars.kv_full[i], 1);
             mbar_init(&bars.kv_empty[i], 2);
@@ -550,25 +585,34 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 prefetch_tmap(&tm_k);
                 prefetch_tmap(&tm_v);
             }
-            int g = 0, it = 0;  // K and V tiles, items
+            int g = 0, q_loads[2] = {0, 0};  // K and V tiles, Q tiles
             bool ok = true;
             const uint32_t q_bytes = 128u * P.group * P.tile_tokens * G::SLABS;
             PaWork w;
-            for (; ok && next_work(w); ++it) {
-                ok = __all_sync(~0u, mbar_wait(&bars.q_empty, (it & 1) ^ 1, wc, kStatusTimeoutSync,
+            const auto load_q = [&](int i) {
+                ok = __all_sync(~0u, mbar_wait(&bars.q_empty[i], (q_loads[i] & 1) ^ 1, wc, kStatusTimeoutSync,
                                                &abort_flag, false));
-                if (!ok) break;
-                const int tiles_q = !ALT && w.n1 > 0 ? 2 : 1;
+                if (!ok) return;
+                ++q_loads[i];
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&bars.q_full, tiles_q * q_bytes);
-                    for (int i = 0; i < tiles_q; ++i)
-                        for (int sl = 0; sl < G::SLABS; ++sl)
-                            tma_load_3d(sQ + i * G::Q_TILE + sl * kSlab, &tm_q, &bars.q_full, sl * 64,
-                                        w.head * P.group, w.q_tok + i * P.tile_tokens);
+                    mbar_arrive_expect_tx(&bars.q_full[i], q_bytes);
+                    for (int sl = 0; sl < G::SLABS; ++sl)
+                        tma_load_3d(sQ + i * G::Q_TILE + sl * kSlab, &tm_q, &bars.q_full[i], sl * 64,
+                                    w.head * P.group, w.q_tok + i * P.tile_tokens);
                 }
+            };
+            while (ok && next_work(w)) {
+                const int tiles_q = ALT ? 1 : (w.n0 > 0 ? 1 : 0) + (w.n1 > 0 ? 2 : 0);  // bits
+                // Q is read once and comes from far: on its way to L2 before its
+                // place is free
+                if (lane < 2 * G::SLABS && ((tiles_q >> (lane & 1)) & 1))
+                    tma_prefetch_3d(&tm_q, (lane >> 1) * 64, w.head * P.group,
+                                    w.q_tok + (lane & 1) * P.tile_tokens);
+                __syncwarp();
+                if (tiles_q & 1) load_q(0);
                 // in the order of use: K0 V0 K1 V1 ..., with two slots of S
-                // K0 K1 V0 K2 V1 ...
-                for (int j = 0; j < 2 * w.n; ++j, ++g) {
+                // K0 K1 V0 K2 V1 ...; the second Q behind the first K
+                for (int j = 0; ok && j < 2 * w.n; ++j) {
                     const bool is_k = SLOTS == 1 ? (j & 1) == 0 : j == 0 || ((j & 1) != 0 && j < 2 * w.n - 1);
                     const int kt = SLOTS == 1 ? j / 2
                                    : is_k     ? (j + 1) / 2
@@ -584,11 +628,15 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                         &bars.kv_full[st], sl * 64, w.head,
                                         w.k_row + (w.lo + kt) * KEYS);
                     }
+                    ++g;
+                    if (j == 0 && (tiles_q & 2)) load_q(1);
                 }
             }
             // drain: the most recent load on every barrier has landed
-            if (it > 0 && lane == 0) {
-                mbar_wait(&bars.q_full, (it - 1) & 1, drain, kStatusTimeoutDrain, nullptr);
+            if (lane == 0) {
+                for (int i = 0; i < 2; ++i)
+                    if (q_loads[i] > 0)
+                        mbar_wait(&bars.q_full[i], (q_loads[i] - 1) & 1, drain, kStatusTimeoutDrain, nullptr);
                 for (int st = 0; st < G::STAGES; ++st) {
                     const int uses = (g - st + G::STAGES - 1) / G::STAGES;  // loads into this stage
                     if (uses > 0)
@@ -703,16 +751,18 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             };
             const auto q_done = [&]() {
-                if (elect_one()) mma_commit(&bars.q_empty);
+                if (elect_one()) mma_commit(&bars.q_empty[ALT ? 0 : x]);
             };
             PaWork w;
             while (ok && next_work(w)) {
-                if (!wait(&bars.q_full, it & 1, kStatusTimeoutLoad)) break;
-                ++it;
                 const int n = __shfl_sync(~0u, w.n, 0);
                 const int nx = ALT ? (n + 1 - x) / 2 : __shfl_sync(~0u, x ? w.n1 : w.n0, 0);
                 const int keys = __shfl_sync(~0u, w.nk - w.lo * KEYS, 0);
-                if (nx == 0 && elect_one()) mbar_arrive(&bars.q_empty);
+                if (ALT || nx > 0) {
+                    if (!wait(&bars.q_full[ALT ? 0 : x], it & 1, kStatusTimeoutLoad)) break;
+                    ++it;
+                }
+                if (ALT && nx == 0 && elect_one()) mbar_arrive(&bars.q_empty[0]);
                 if constexpr (!ALT) {
                     // the first S; then per key tile: P V, and S in the slot it frees
                     for (int j = 0; j < SLOTS && j < n; ++j) {
@@ -787,9 +837,74 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                              (SLOTS == 2 ? k >> 1 : k) & 1, wc, kStatusTimeoutMma,
                                              &abort_flag, false));
         };
-        PaWork w;
-        bool ok = true;
-        while (ok && next_work(w)) {
+        // What is to be written of the item before: its rows are written once the
+        // last P V is complete, which the next item's first S comes behind; O is
+        // free for the next P V once it is in registers.
+        struct Due {
+            bool live, valid;
+            float m, l;
+            int token, head, slot;
+        } due{};
+        bool is_due = false;
+        PaWork w{};
+        bool ok = true, more = true;
+        while (more) {
+            more = next_work(w);
+            if (is_due) {
+                is_due = false;
+                if (!(ok = pv_over())) break;
+                tc_fence_after();
+                const float l = due.l, inv = l == 0.f ? 0.f : 1.f / l;
+                const int64_t at = (static_cast<int64_t>(due.slot) * 2 + x) * P.ws_rows + row;
+                const int64_t token = due.token, head = static_cast<int64_t>(due.head) * P.group + hd;
+                char *mine = PIECES ? reinterpret_cast<char *>(P.ws_o + at * D)
+                                    : reinterpret_cast<char *>(static_cast<T *>(P.out) +
+                                                               token * P.out_token + head * P.out_head);
+                char *rows[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    rows[i] = reinterpret_cast<char *>(
+                        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine), (lane & ~3) + i));
+                const unsigned rows_ok = __ballot_sync(~0u, due.valid) >> (lane & ~3);
+                constexpr int COLS = PIECES ? 16 : 32;  // 64 bytes
+#pragma unroll 1
+                for (int q = 0; q < D; q += COLS) {
+                    uint32_t v[16];
+                    if (due.live) {
+                        if constexpr (PIECES) {
+                            tmem_ld16(tO + q, v);
+                            tmem_ld_wait(v);
+                        } else {
+                            uint32_t o[32];
+                            tmem_ld32(tO + q, o);
+                            tmem_ld_wait(o);
+                            // a row that sees no key (or only scores of -inf) gives zeros
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                v[e] = l == 0.f ? 0u
+                                                : pa_pack<T>(__uint_as_float(o[2 * e]) * inv,
+                                                             __uint_as_float(o[2 * e + 1]) * inv);
+                        }
+                    }
+                    if (q == D - COLS) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.o_empty[x]);
+                    }
+                    if (due.live)
+                        store_rows(v, rows, q * (PIECES ? 4 : 2), rows_ok,
+                                   q + (lane & 3) * (COLS / 4) < P.d, lane);
+                }
+                if (due.valid) {
+                    if constexpr (PIECES) {
+                        P.ws_ml[at] = make_float2(due.m, l);
+                    } else if (P.lse != nullptr) {
+                        P.lse[token * P.group * P.heads_kv + head] =
+                            l == 0.f ? -INFINITY : (due.m + __log2f(l)) * 0.69314718055994531f;
+                    }
+                }
+            }
+            if (!more) break;
             const int n = ALT ? (w.n + 1 - x) / 2 : (x ? w.n1 : w.n0);
             const int shift_tok = ALT ? 0 : x * P.tile_tokens;
             const int toks = min(w.toks - shift_tok, P.tile_tokens);  // of this tile
@@ -849,14 +964,18 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     while (true) {
                         if (__any_sync(~0u, own || m_next > m)) {
                             if (__any_sync(~0u, own)) {
-                                float mx = -INFINITY;
+                                float mx[NC];
 #pragma unroll
-                                for (int q = 0; q < NC; ++q)
+                                for (int q = 0; q < NC; ++q) {
+                                    mx[q] = -INFINITY;
 #pragma unroll
                                     for (int e = 0; e < 32; e += 2)
-                                        mx = fmax3(mx, __uint_as_float(s[q][e]),
-                                                   __uint_as_float(s[q][e + 1]));
-                                if (own) m_next = fmaxf(m, mx * c);
+                                        mx[q] = fmax3(mx[q], __uint_as_float(s[q][e]),
+                                                      __uint_as_float(s[q][e + 1]));
+                                }
+                                float top = fmax3(mx[0], mx[1], mx[2]);
+                                if constexpr (NC == 4) top = fmaxf(top, mx[3]);
+                                if (own) m_next = fmaxf(m, top * c);
                             }
                             const float alpha = m_next > m ? (m == -INFINITY ? 0.f : ex2_approx(m - m_next)) : 1.f;
                             m = m_next;
@@ -918,63 +1037,17 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!ok) break;
             g += 2 * w.n;
             if (n > 0) {
-                ok = pv_over();
-                if (!ok) break;
-                tc_fence_after();
-            }
-            if constexpr (PIECES) {
-                const int64_t at = (static_cast<int64_t>(w.slot) * 2 + x) * P.ws_rows + row;
-                const bool mine = valid && row < P.ws_rows;
-                if (mine) P.ws_ml[at] = make_float2(n > 0 ? m : -INFINITY, n > 0 ? l : 0.f);
-                if (warp_live && n > 0) {
-                    float *dst = P.ws_o + at * D;
-#pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + q * 32, o);
-                        tmem_ld_wait(o);
-                        if (mine)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<uint4 *>(dst + q * 32 + e) =
-                                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    }
-                }
-            } else if (warp_live && n > 0) {
-                // a row that sees no key (or only scores of -inf) gives zeros
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                const int64_t token = w.q_tok + shift_tok + tok;
-                const int64_t head = static_cast<int64_t>(w.head) * P.group + hd;
-                T *dst = static_cast<T *>(P.out) + token * P.out_token + head * P.out_head;
-                if (valid && P.lse != nullptr)
-                    P.lse[token * P.group * P.heads_kv + head] =
-                        l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
-#pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + q * 32, o);
-                    tmem_ld_wait(o);
-                    if (valid) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            if (q * 32 + e < P.d) {
-                                uint32_t v[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const float a = __uint_as_float(o[e + 2 * k]) * inv;
-                                    const float b = __uint_as_float(o[e + 2 * k + 1]) * inv;
-                                    v[k] = l == 0.f ? 0u : pa_pack<T>(a, b);
-                                }
-                                *reinterpret_cast<uint4 *>(dst + q * 32 + e) =
-                                    make_uint4(v[0], v[1], v[2], v[3]);
-                            }
-                    }
-                }
-            }
-            if (n > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.o_empty[x]);
+                due.live = warp_live;
+                due.valid = valid && (!PIECES || row < P.ws_rows);
+                due.m = m;
+                due.l = l;
+                due.token = w.q_tok + shift_tok + tok;
+                due.head = w.head;
+                due.slot = w.slot;
+                is_due = true;
+            } else if (PIECES && valid && row < P.ws_rows) {
+                P.ws_ml[(static_cast<int64_t>(w.slot) * 2 + x) * P.ws_rows + row] =
+                    make_float2(-INFINITY, 0.f);
             }
         }
     }

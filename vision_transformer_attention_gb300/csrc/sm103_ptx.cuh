@@ -196,6 +196,13 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *m, uin
         : "memory");
 }
 
+// A box on its way to L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *m, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 // Store a box from shared memory; coordinates must be >= 0 (out-of-range
 // parts of the box past the tensor's end are not written).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, const void *src, int c0,
