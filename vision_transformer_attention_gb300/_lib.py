@@ -6,10 +6,12 @@ or pure-PyTorch stand-in for any entry point.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libvta_gb300.so")
+BIND_PATH = os.path.join(_PKG, "_build", "vta_bind.so")
 
 RPE_OK = 0
 RPE_ERR_INVALID_ARG = 1
@@ -91,6 +93,31 @@ def lib():
             fn.argtypes = args
         _lib = handle
     return _lib
+
+
+class _NoBind:
+    """Stands for vta_bind where it cannot be loaded: nothing is done the quick way."""
+    rope = attn = staticmethod(lambda *args: None)
+
+
+_bind = None
+
+
+def bind():
+    """The extension module that makes the calls on tokens straight from tensor objects
+    (csrc/bind.cpp); its functions return None for a call that they leave to api.py."""
+    global _bind
+    if _bind is None:
+        lib()
+        try:
+            import torch  # noqa: F401  (its libraries are what the module links against)
+            spec = importlib.util.spec_from_file_location("vta_bind", BIND_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _bind = module
+        except (ImportError, OSError, AttributeError):
+            _bind = _NoBind
+    return _bind
 
 
 def check(fn, status):

@@ -183,8 +183,7 @@ def swin_window_attn_fwd_fmap(q, k, v, bias_table, M, out=None):
 
 def _call(t, name, *args):
     """Calls the entry point with t's device current and that device's current stream as the
-    last argument. (The device guard and the stream object cost as much as a small kernel, so
-    the guard is entered only where the device differs.)"""
+    last argument."""
     fn = getattr(_lib.lib(), name)
     device = t.get_device()
     if device == torch.cuda.current_device():
@@ -289,6 +288,11 @@ def rope_fwd(q, k, positions, phases, interleaved=False, inverse=False, magnitud
     k_out may be q and k. Returns (q_out, k_out or None)."""
     if phases is None:
         raise ValueError("phases must be a table of rope_build_phases")
+    done = _lib.bind().rope(q, k, q_out, k_out, positions, phases,
+                            (_lib.RPE_ROPE_INTERLEAVED if interleaved else 0) |
+                            (_lib.RPE_ROPE_INVERSE if inverse else 0), magnitude, -1, 0.0, None, None)
+    if done is not None:
+        return done
     q_out, k_out, views, rest = _rope_args(q, k, positions, phases, interleaved, inverse,
                                            magnitude, q_out, k_out)
     _call(q, "rope_fwd", *views, *rest)
@@ -300,6 +304,11 @@ def qk_norm_rope_fwd(q, k, q_gain, k_gain, positions=None, phases=None, norm=_li
     """The norm of each head of q and k (RPE_NORM_RMS or RPE_NORM_LAYER, gains [d] of q's
     type or float32, None: ones) and the rotation of rope_fwd (phases None: no rotation) in
     one pass. Returns (q_out, k_out or None)."""
+    done = _lib.bind().rope(q, k, q_out, k_out, positions, phases,
+                            _lib.RPE_ROPE_INTERLEAVED if interleaved else 0, magnitude, norm, eps,
+                            q_gain, k_gain)
+    if done is not None:
+        return done
     q_out, k_out, views, rest = _rope_args(q, k, positions, phases, interleaved, False,
                                            magnitude, q_out, k_out)
     gain_dtype, ptrs = None, [None, None]
@@ -332,6 +341,9 @@ def packed_attn_fwd(q, k, v, cu_q, cu_k=None, k_lens=None, causal=False, scale=N
     out that belong to no sequence stay as they were. workspace: a uint8 tensor of at least
     packed_attn_workspace bytes (None: one is allocated for the call). Returns out, or
     (out, lse [total_q, heads_q]) with return_lse."""
+    done = _lib.bind().attn(q, k, v, cu_q, cu_k, k_lens, causal, scale, out, return_lse, workspace)
+    if done is not None:
+        return done
     qv = _view(q, "q")
     dtype, device, shape = q.dtype, q.device, q.shape
     if len(shape) != 3:
