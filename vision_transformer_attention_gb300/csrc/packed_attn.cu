@@ -16,7 +16,7 @@ struct Plan {
     int kind;  // 0 whole items, 1 pieces of two tiles, 2 pieces of one
     int ctas, tile_tokens, ws_rows;
     int64_t max_items;
-    size_t ml_at, o_at, bytes;  // workspace offsets and size (pieces)
+    size_t item_at, ml_at, o_at, bytes;  // workspace offsets and size (pieces)
 };
 
 int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
@@ -41,7 +41,8 @@ Plan make_plan(int64_t total_q, int64_t total_k, int batch, int heads_q, int hea
     p.ws_rows = static_cast<int>(least(128, group * least(p.tile_tokens, total_q)));
     const int D = d <= 64 ? 64 : 128;
     const size_t rows = static_cast<size_t>(p.max_items + p.ctas) * 2 * p.ws_rows;
-    p.ml_at = 64 + static_cast<size_t>(p.max_items) * 32;
+    p.item_at = 64 + static_cast<size_t>(p.max_items) * 32;
+    p.ml_at = (p.item_at + static_cast<size_t>(total_q) * sizeof(int32_t) + 127) & ~static_cast<size_t>(127);
     p.o_at = (p.ml_at + rows * sizeof(float2) + 127) & ~static_cast<size_t>(127);
     p.bytes = p.o_at + rows * D * sizeof(float);
     return p;
@@ -123,7 +124,8 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     const Plan p = make_plan(total_q, total_k, batch, heads_q, heads_kv, d);
     if (p.bytes > 0 && (workspace == nullptr || !aligned(workspace, 128) || workspace_bytes < p.bytes))
         return RPE_ERR_INVALID_ARG;
-    if (2 * p.max_items * p.ws_rows > INT32_MAX) return RPE_ERR_UNSUPPORTED;
+    if (p.kind && (p.max_items > INT32_MAX / 2 || total_q * heads_q > INT32_MAX))
+        return RPE_ERR_UNSUPPORTED;
 
     PackedAttnArgs a{};
     a.cu_q = cu_q;
@@ -145,6 +147,7 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     if (p.kind) {
         char *ws = static_cast<char *>(workspace);
         a.workspace = ws;
+        a.ws_item = reinterpret_cast<int32_t *>(ws + p.item_at);
         a.ws_ml = reinterpret_cast<float2 *>(ws + p.ml_at);
         a.ws_o = reinterpret_cast<float *>(ws + p.o_at);
         a.ws_rows = p.ws_rows;

@@ -92,7 +92,7 @@ struct PaWork {
 };
 
 struct PaBars {
-    uint64_t q_full[2], q_empty[2];  // alternate: only the first
+    uint64_t q_full[2], q_empty[2];  // of a tile; alternate: of every other item
     uint64_t kv_full[15], kv_empty[15];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // tile, slot
     uint64_t o_empty[2];
@@ -451,10 +451,14 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
         w.n0 = min(max(kt0 - lo, 0), n);
         w.n1 = w.toks > P.tile_tokens ? n : 0;
         w.slot = item + h + blockIdx.x;
-        if (lo == 0 && lane == 0) {
-            meta[2 * (item + h)] = make_int4(static_cast<int>(first & 0xFFFFFFFFll),
-                                             static_cast<int>(first >> 32), kt, w.q_tok);
-            meta[2 * (item + h) + 1] = make_int4(w.toks, h, 0, 0);
+        if (lo == 0) {  // for the kernel that joins the pieces: the item, and its tokens' item
+            if (lane == 0) {
+                meta[2 * (item + h)] = make_int4(static_cast<int>(first & 0xFFFFFFFFll),
+                                                 static_cast<int>(first >> 32), kt, w.q_tok);
+                meta[2 * (item + h) + 1] = make_int4(w.toks, h, 0, 0);
+            }
+            if (h == 0)
+                for (int i = lane; i < w.toks; i += 32) P.ws_item[w.q_tok + i] = item;
         }
         if (!ring.put(w, lane)) return;
         u += n;
@@ -589,7 +593,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             bool ok = true;
             const uint32_t q_bytes = 128u * P.group * P.tile_tokens * G::SLABS;
             PaWork w;
-            const auto load_q = [&](int i) {
+            const auto load_q = [&](int i, int tok) {  // into buffer i
                 ok = __all_sync(~0u, mbar_wait(&bars.q_empty[i], (q_loads[i] & 1) ^ 1, wc, kStatusTimeoutSync,
                                                &abort_flag, false));
                 if (!ok) return;
@@ -598,9 +602,10 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mbar_arrive_expect_tx(&bars.q_full[i], q_bytes);
                     for (int sl = 0; sl < G::SLABS; ++sl)
                         tma_load_3d(sQ + i * G::Q_TILE + sl * kSlab, &tm_q, &bars.q_full[i], sl * 64,
-                                    w.head * P.group, w.q_tok + i * P.tile_tokens);
+                                    w.head * P.group, w.q_tok + tok);
                 }
             };
+            int it = 0;
             while (ok && next_work(w)) {
                 const int tiles_q = ALT ? 1 : (w.n0 > 0 ? 1 : 0) + (w.n1 > 0 ? 2 : 0);  // bits
                 // Q is read once and comes from far: on its way to L2 before its
@@ -609,9 +614,9 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tma_prefetch_3d(&tm_q, (lane >> 1) * 64, w.head * P.group,
                                     w.q_tok + (lane & 1) * P.tile_tokens);
                 __syncwarp();
-                if (tiles_q & 1) load_q(0);
                 // in the order of use: K0 V0 K1 V1 ..., with two slots of S
-                // K0 K1 V0 K2 V1 ...; the second Q behind the first K
+                // K0 K1 V0 K2 V1 ...; Q behind the first two, whose places are free
+                // before Q's is
                 for (int j = 0; ok && j < 2 * w.n; ++j) {
                     const bool is_k = SLOTS == 1 ? (j & 1) == 0 : j == 0 || ((j & 1) != 0 && j < 2 * w.n - 1);
                     const int kt = SLOTS == 1 ? j / 2
@@ -629,7 +634,14 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                         w.k_row + (w.lo + kt) * KEYS);
                     }
                     ++g;
-                    if (j == 0 && (tiles_q & 2)) load_q(1);
+                    if (j == 1) {
+                        if (ALT) {
+                            load_q(it++ & 1, 0);
+                        } else {
+                            if (tiles_q & 1) load_q(0, 0);
+                            if (ok && (tiles_q & 2)) load_q(1, P.tile_tokens);
+                        }
+                    }
                 }
             }
             // drain: the most recent load on every barrier has landed
@@ -650,7 +662,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const int x = warp - kWarpMma;
             const uint32_t hi = static_cast<uint32_t>(smem_desc(0, 0, 1024, kSwizzle128B) >> 32);
             constexpr uint32_t kLboK = (16u >> 4) << 16, kLboV = static_cast<uint32_t>(G::KV_SLAB >> 4) << 16;
-            const uint32_t aQ = ((smem_u32(sQ) + (ALT ? 0 : x) * G::Q_TILE) >> 4) | kLboK;
+            uint32_t aQ = ((smem_u32(sQ) + (ALT ? 0 : x) * G::Q_TILE) >> 4) | kLboK;
             const uint32_t aKV = smem_u32(sKV) >> 4;
             const uint32_t t0 = __shfl_sync(~0u, tmem, 0);
             const uint32_t tS0 = t0 + G::S_COL + x * KEYS * G::SLOTS, tO = t0 + G::O_COL + x * D;
@@ -751,18 +763,22 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             };
             const auto q_done = [&]() {
-                if (elect_one()) mma_commit(&bars.q_empty[ALT ? 0 : x]);
+                if (elect_one()) mma_commit(&bars.q_empty[ALT ? (it - 1) & 1 : x]);
             };
             PaWork w;
             while (ok && next_work(w)) {
                 const int n = __shfl_sync(~0u, w.n, 0);
                 const int nx = ALT ? (n + 1 - x) / 2 : __shfl_sync(~0u, x ? w.n1 : w.n0, 0);
                 const int keys = __shfl_sync(~0u, w.nk - w.lo * KEYS, 0);
-                if (ALT || nx > 0) {
-                    if (!wait(&bars.q_full[ALT ? 0 : x], it & 1, kStatusTimeoutLoad)) break;
+                if (ALT) {  // every other item's Q in the other buffer
+                    if (!wait(&bars.q_full[it & 1], (it >> 1) & 1, kStatusTimeoutLoad)) break;
+                    aQ = ((smem_u32(sQ) + (it & 1) * G::Q_TILE) >> 4) | kLboK;
+                    if (nx == 0 && elect_one()) mbar_arrive(&bars.q_empty[it & 1]);
+                    ++it;
+                } else if (nx > 0) {
+                    if (!wait(&bars.q_full[x], it & 1, kStatusTimeoutLoad)) break;
                     ++it;
                 }
-                if (ALT && nx == 0 && elect_one()) mbar_arrive(&bars.q_empty[0]);
                 if constexpr (!ALT) {
                     // the first S; then per key tile: P V, and S in the slot it frees
                     for (int j = 0; j < SLOTS && j < n; ++j) {
@@ -857,43 +873,64 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const float l = due.l, inv = l == 0.f ? 0.f : 1.f / l;
                 const int64_t at = (static_cast<int64_t>(due.slot) * 2 + x) * P.ws_rows + row;
                 const int64_t token = due.token, head = static_cast<int64_t>(due.head) * P.group + hd;
-                char *mine = PIECES ? reinterpret_cast<char *>(P.ws_o + at * D)
-                                    : reinterpret_cast<char *>(static_cast<T *>(P.out) +
-                                                               token * P.out_token + head * P.out_head);
-                char *rows[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    rows[i] = reinterpret_cast<char *>(
-                        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine), (lane & ~3) + i));
-                const unsigned rows_ok = __ballot_sync(~0u, due.valid) >> (lane & ~3);
-                constexpr int COLS = PIECES ? 16 : 32;  // 64 bytes
+                if constexpr (ALT) {
+                    // few rows: 128 bytes of each per thread and step, no exchange
+                    float *dst = P.ws_o + at * D;
 #pragma unroll 1
-                for (int q = 0; q < D; q += COLS) {
-                    uint32_t v[16];
-                    if (due.live) {
-                        if constexpr (PIECES) {
-                            tmem_ld16(tO + q, v);
-                            tmem_ld_wait(v);
-                        } else {
-                            uint32_t o[32];
+                    for (int q = 0; q < D; q += 32) {
+                        uint32_t o[32];
+                        if (due.live) {
                             tmem_ld32(tO + q, o);
                             tmem_ld_wait(o);
-                            // a row that sees no key (or only scores of -inf) gives zeros
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                v[e] = l == 0.f ? 0u
-                                                : pa_pack<T>(__uint_as_float(o[2 * e]) * inv,
-                                                             __uint_as_float(o[2 * e + 1]) * inv);
                         }
+                        if (due.valid)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<uint4 *>(dst + q + e) =
+                                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
-                    if (q == D - COLS) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars.o_empty[x]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.o_empty[x]);
+                } else {
+                    char *mine = PIECES ? reinterpret_cast<char *>(P.ws_o + at * D)
+                                        : reinterpret_cast<char *>(static_cast<T *>(P.out) +
+                                                                   token * P.out_token + head * P.out_head);
+                    char *rows[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        rows[i] = reinterpret_cast<char *>(
+                            __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine), (lane & ~3) + i));
+                    const unsigned rows_ok = __ballot_sync(~0u, due.valid) >> (lane & ~3);
+                    constexpr int COLS = PIECES ? 16 : 32;  // 64 bytes
+#pragma unroll 1
+                    for (int q = 0; q < D; q += COLS) {
+                        uint32_t v[16];
+                        if (due.live) {
+                            if constexpr (PIECES) {
+                                tmem_ld16(tO + q, v);
+                                tmem_ld_wait(v);
+                            } else {
+                                uint32_t o[32];
+                                tmem_ld32(tO + q, o);
+                                tmem_ld_wait(o);
+                                // a row that sees no key (or only scores of -inf) gives zeros
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    v[e] = l == 0.f ? 0u
+                                                    : pa_pack<T>(__uint_as_float(o[2 * e]) * inv,
+                                                                 __uint_as_float(o[2 * e + 1]) * inv);
+                            }
+                        }
+                        if (q == D - COLS) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars.o_empty[x]);
+                        }
+                        if (due.live)
+                            store_rows(v, rows, q * (PIECES ? 4 : 2), rows_ok,
+                                       q + (lane & 3) * (COLS / 4) < P.d, lane);
                     }
-                    if (due.live)
-                        store_rows(v, rows, q * (PIECES ? 4 : 2), rows_ok,
-                                   q + (lane & 3) * (COLS / 4) < P.d, lane);
                 }
                 if (due.valid) {
                     if constexpr (PIECES) {
@@ -1059,9 +1096,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-// Joins the pieces of the tiles: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p.
+// Joins the pieces of the rows: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p.
 // WIDE: a CTA per row, its warps taking every eighth piece (few rows, many
-// pieces); otherwise a warp per row.
+// pieces); otherwise a warp per row. Rows of no sequence are left alone: their
+// entry of ws_item is whatever the workspace held, which is believed only if the
+// item it names says that it holds the row.
 constexpr int kJoinWarps = 8;
 
 template <typename T, int D, bool ALT, bool WIDE>
@@ -1070,19 +1109,21 @@ packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int grid) {
     constexpr int C = D / 32;  // columns per lane
     __shared__ float part[WIDE ? kJoinWarps : 1][WIDE ? D : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = (ALT ? 1 : 2) * P.ws_rows;  // of an item
-    const int blocks = WIDE ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
-    const int item = blockIdx.x / blocks;
-    const int item_row = WIDE ? blockIdx.x - item * blocks : (blockIdx.x - item * blocks) * kJoinWarps + warp;
-    const int x = !ALT && item_row >= P.ws_rows ? 1 : 0, row = item_row - x * P.ws_rows;
+    const int64_t out_row = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
+    const int heads = P.group * P.heads_kv;
+    const int64_t token = out_row / heads;
+    if (token >= P.total_q) return;
+    const int out_head = static_cast<int>(out_row - token * heads), kv_head = out_head / P.group;
     griddep_wait();
     const int *header = static_cast<const int *>(P.workspace);
     const long long all = *reinterpret_cast<const long long *>(header);
-    if (item >= header[2] || item_row >= rows) return;
+    const int count = header[2], item = P.ws_item[token] + kv_head;
+    if (item < kv_head || item >= count) return;
     const int4 *meta = reinterpret_cast<const int4 *>(header + 16) + 2 * item;
     const int4 a = meta[0], b = meta[1];
-    const int tile_tok = row / P.group, tok = x * P.tile_tokens + tile_tok;
-    if (tile_tok >= P.tile_tokens || tok >= b.x) return;
+    if (token < a.w || token >= a.w + b.x || b.y != kv_head) return;
+    const int tok = static_cast<int>(token - a.w), x = tok >= P.tile_tokens ? 1 : 0;
+    const int row = (tok - x * P.tile_tokens) * P.group + (out_head - kv_head * P.group);
     const long long first = (static_cast<long long>(a.y) << 32) | static_cast<uint32_t>(a.x);
     const long long ctas = all < grid ? all : grid;
     const int c0 = static_cast<int>(((first + 1) * ctas - 1) / all);
@@ -1135,13 +1176,11 @@ packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int grid) {
         }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t token = a.w + tok;
-    const int64_t head = static_cast<int64_t>(b.y) * P.group + (row - tile_tok * P.group);
     if (lane == 0 && P.lse != nullptr)
-        P.lse[token * P.group * P.heads_kv + head] =
+        P.lse[out_row] =
             L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
     if (lane * C >= P.d) return;
-    T *dst = static_cast<T *>(P.out) + token * P.out_token + head * P.out_head + lane * C;
+    T *dst = static_cast<T *>(P.out) + token * P.out_token + out_head * P.out_head + lane * C;
 #pragma unroll
     for (int e = 0; e < C; ++e) acc[e] = L == 0.f ? 0.f : acc[e] * inv;
     if constexpr (C == 4)
@@ -1163,15 +1202,13 @@ cudaError_t pa_launch_kind(const PackedAttnMaps &m, const PackedAttnArgs &a, int
     if constexpr (KIND != kWhole) {
         if (err != cudaSuccess) return err;
         constexpr bool ALT = KIND == kAlternate;
-        const int rows = (ALT ? 1 : 2) * a.ws_rows;
-        const int64_t all = static_cast<int64_t>(a.max_items) * rows;
-        if (all <= 16 * sm_count())
-            return launch_pdl(packed_combine_kernel<T, D, ALT, true>, dim3(static_cast<unsigned>(all)),
+        const int64_t rows = static_cast<int64_t>(a.total_q) * a.group * a.heads_kv;
+        if (rows <= 4 * sm_count())
+            return launch_pdl(packed_combine_kernel<T, D, ALT, true>, dim3(static_cast<unsigned>(rows)),
                               dim3(32 * kJoinWarps), 0, stream, a, ctas);
-        const int blocks = (rows + kJoinWarps - 1) / kJoinWarps;
         return launch_pdl(packed_combine_kernel<T, D, ALT, false>,
-                          dim3(static_cast<unsigned>(a.max_items) * blocks), dim3(32 * kJoinWarps),
-                          0, stream, a, ctas);
+                          dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),
+                          dim3(32 * kJoinWarps), 0, stream, a, ctas);
     }
     return err;
 }

@@ -176,9 +176,11 @@ struct PackedAttnArgs {
     void *out;
     int64_t out_token, out_head;
     float *lse;  // [total_q, heads_q] or NULL
-    // pieces: the workspace (a header, two int4 per item), the row maxima and
-    // sums, the unnormalised outputs [slot][2][ws_rows][D]
+    // pieces: the workspace (a header, two int4 per item), each token's first
+    // item, the row references and sums, the unnormalised outputs
+    // [slot][2][ws_rows][D]
     void *workspace;
+    int32_t *ws_item;
     float2 *ws_ml;
     float *ws_o;
     int ws_rows, max_items;
