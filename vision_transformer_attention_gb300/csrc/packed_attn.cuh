@@ -79,6 +79,30 @@ struct PaGeo {
     static constexpr uint32_t O_COL = D == 64 ? 0 : 256, S_COL = D == 64 ? 128 : 0;
 };
 
+// The waits of the warps that load, issue and schedule. Out of line (but for the
+// first try) for D = 128, where some twenty loops in line make the code of a tile
+// outgrow the instruction cache (long causal prompts 396 us, 385 out of line); in
+// line for D = 64, whose waits are more and mostly not over at the first try
+// (images 188 us, 196 out of line).
+struct PaWait {
+    unsigned *status;
+    volatile int *abort;
+};
+__device__ __noinline__ bool pa_wait_on(uint64_t *bar, uint32_t parity, unsigned code, unsigned *status,
+                                        volatile int *abort) {
+    return mbar_wait(bar, parity, WaitCtl{status, kDefaultWaitNs}, code, abort, false);
+}
+template <int D>
+__device__ __forceinline__ bool pa_wait(uint64_t *bar, uint32_t parity, unsigned code, const PaWait &w) {
+    if constexpr (D == 64) return mbar_wait(bar, parity, WaitCtl{w.status, kDefaultWaitNs}, code, w.abort, false);
+    return mbar_try_wait(bar, parity) || pa_wait_on(bar, parity, code, w.status, w.abort);
+}
+
+// In line altogether: for the softmax warps, which hold too much for a call.
+__device__ __forceinline__ bool pa_wait_in(uint64_t *bar, uint32_t parity, unsigned code, const PaWait &w) {
+    return mbar_wait(bar, parity, WaitCtl{w.status, kDefaultWaitNs}, code, w.abort, false);
+}
+
 // One unit of work, as the schedule warp hands it to the others.
 struct PaWork {
     int q_tok;  // first token of the first tile (of all tokens)
@@ -238,17 +262,17 @@ __device__ __forceinline__ void store_rows(uint32_t (&v)[16], char *const (&rows
 // ------------------------------------------------------------- schedule
 
 // Hands PaWork entries to the other roles through a ring in shared memory.
+template <int D>
 struct PaRing {
     PaWork *slots;
     uint64_t *full, *empty;
-    const WaitCtl *wc;
-    volatile int *abort;
+    PaWait wc;
     int n = 0;
     // Called by the whole warp with the same values; false: give up.
     __device__ __forceinline__ bool put(const PaWork &w, int lane) {
         const int s = n % kWorkSlots, use = n / kWorkSlots;
         ++n;
-        if (!__all_sync(~0u, mbar_wait(&empty[s], (use & 1) ^ 1, *wc, kStatusTimeoutSync, abort)))
+        if (!__all_sync(~0u, pa_wait<D>(&empty[s], (use & 1) ^ 1, kStatusTimeoutSync, wc)))
             return false;
         if (lane == 0) {
             slots[s] = w;
@@ -261,8 +285,8 @@ struct PaRing {
 
 // Whole items, the costliest first (by key tiles, in at most 64 levels), dealt
 // to the CTAs round by round, every other round backwards.
-template <int KEYS>
-__device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRing ring, int lane,
+template <int KEYS, int D>
+__device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRing<D> ring, int lane,
                                                   int most_tiles) {
     const int TT = 2 * P.tile_tokens;
     int shift = 0;
@@ -348,8 +372,8 @@ __device__ __forceinline__ void pa_units(const PackedAttnArgs &P, const PaSeq &s
 
 // Shared and alternate: this CTA's share [u0, u1) of all units, in (sequence,
 // tokens, head, key tile) order. per: sequences per warp of the count before.
-template <int KEYS>
-__device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRing ring, int lane,
+template <int KEYS, int D>
+__device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRing<D> ring, int lane,
                                                    int TT, const long long *warp_units,
                                                    const int *warp_tiles, int per) {
     long long all = 0;
@@ -485,8 +509,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(~0u, tid >> 5, 0);  // the same in all lanes
-    const WaitCtl wc{P.status, kDefaultWaitNs};
-    const WaitCtl drain{P.status, kDefaultWaitNs};
+    const PaWait wc{P.status, &abort_flag}, drain{P.status, nullptr};
     uint8_t *sQ = pa_smem, *sKV = pa_smem + 2 * G::Q_TILE;
 
     if (tid == 0) {
@@ -564,7 +587,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const auto next_work = [&](PaWork &w) -> bool {  // by the whole warp
         const int s = wn % kWorkSlots, use = wn / kWorkSlots;
         ++wn;
-        if (!__all_sync(~0u, mbar_wait(&bars.w_full[s], use & 1, wc, kStatusTimeoutSync, &abort_flag, false)))
+        if (!__all_sync(~0u, pa_wait_in(&bars.w_full[s], use & 1, kStatusTimeoutSync, wc)))
             return false;
         w = work[s];
         __syncwarp();
@@ -575,13 +598,13 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp >= 8) {
         regs_dealloc<kPaRegsControl>();
         if (warp == kWarpSched) {
-            PaRing ring{work, bars.w_full, bars.w_empty, &wc, &abort_flag};
+            PaRing<D> ring{work, bars.w_full, bars.w_empty, wc};
             if constexpr (PIECES) {
-                pa_schedule_pieces<KEYS>(P, ring, lane, TT, warp_units, warp_tiles, per);
+                pa_schedule_pieces<KEYS, D>(P, ring, lane, TT, warp_units, warp_tiles, per);
             } else {
                 int most = 1;
                 for (int i = 0; i < kPaThreads / 32; ++i) most = max(most, warp_tiles[i]);
-                pa_schedule_items<KEYS>(P, ring, lane, most);
+                pa_schedule_items<KEYS, D>(P, ring, lane, most);
             }
         } else if (warp == kWarpLoad) {
             if (lane == 0) {
@@ -594,8 +617,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const uint32_t q_bytes = 128u * P.group * P.tile_tokens * G::SLABS;
             PaWork w;
             const auto load_q = [&](int i, int tok) {  // into buffer i
-                ok = __all_sync(~0u, mbar_wait(&bars.q_empty[i], (q_loads[i] & 1) ^ 1, wc, kStatusTimeoutSync,
-                                               &abort_flag, false));
+                ok = __all_sync(~0u, pa_wait<D>(&bars.q_empty[i], (q_loads[i] & 1) ^ 1, kStatusTimeoutSync, wc));
                 if (!ok) return;
                 ++q_loads[i];
                 if (lane == 0) {
@@ -623,8 +645,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                    : is_k     ? (j + 1) / 2
                                               : (j == 2 * w.n - 1 ? w.n - 1 : j / 2 - 1);
                     const int st = g % G::STAGES, use = g / G::STAGES;
-                    ok = __all_sync(~0u, mbar_wait(&bars.kv_empty[st], (use & 1) ^ 1, wc,
-                                                   kStatusTimeoutSync, &abort_flag, false));
+                    ok = __all_sync(~0u, pa_wait<D>(&bars.kv_empty[st], (use & 1) ^ 1, kStatusTimeoutSync, wc));
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bars.kv_full[st], G::TILE);
@@ -648,11 +669,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (lane == 0) {
                 for (int i = 0; i < 2; ++i)
                     if (q_loads[i] > 0)
-                        mbar_wait(&bars.q_full[i], (q_loads[i] - 1) & 1, drain, kStatusTimeoutDrain, nullptr);
+                        pa_wait<D>(&bars.q_full[i], (q_loads[i] - 1) & 1, kStatusTimeoutDrain, drain);
                 for (int st = 0; st < G::STAGES; ++st) {
                     const int uses = (g - st + G::STAGES - 1) / G::STAGES;  // loads into this stage
                     if (uses > 0)
-                        mbar_wait(&bars.kv_full[st], (uses - 1) & 1, drain, kStatusTimeoutDrain, nullptr);
+                        pa_wait<D>(&bars.kv_full[st], (uses - 1) & 1, kStatusTimeoutDrain, drain);
                 }
             }
             __syncwarp();
@@ -675,7 +696,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             bool ok = true;
 
             const auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code) {
-                ok = ok && __all_sync(~0u, mbar_wait(bar, parity, wc, code, &abort_flag, false));
+                ok = ok && __all_sync(~0u, pa_wait<D>(bar, parity, code, wc));
                 return ok;
             };
             const auto kv_wait = [&]() { return wait(&bars.kv_full[st], ph, kStatusTimeoutLoad); };
@@ -829,7 +850,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             __syncwarp();
             if (elect_one()) {
                 mma_commit(&bars.fin[x]);
-                mbar_wait(&bars.fin[x], 0, drain, kStatusTimeoutDrain, nullptr);
+                pa_wait<D>(&bars.fin[x], 0, kStatusTimeoutDrain, drain);
             }
         }
         __syncwarp();
@@ -849,9 +870,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // none after it can be: the phase is unambiguous.)
         const auto pv_over = [&]() {
             const int k = ns - 1;
-            return __all_sync(~0u, mbar_wait(&bars.pv_done[x][SLOTS == 2 ? k & 1 : 0],
-                                             (SLOTS == 2 ? k >> 1 : k) & 1, wc, kStatusTimeoutMma,
-                                             &abort_flag, false));
+            return __all_sync(~0u, pa_wait_in(&bars.pv_done[x][SLOTS == 2 ? k & 1 : 0], (SLOTS == 2 ? k >> 1 : k) & 1, kStatusTimeoutMma, wc));
         };
         // What is to be written of the item before: its rows are written once the
         // last P V is complete, which the next item's first S comes behind; O is
@@ -956,8 +975,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int i = 0; i < n; ++i, ++ns) {
                 const int j = ALT ? 2 * i + x : i, kt = w.lo + j;
                 const int sl = SLOTS == 2 ? ns & 1 : 0;
-                ok = __all_sync(~0u, mbar_wait(&bars.s_full[x][sl], (SLOTS == 2 ? ns >> 1 : ns) & 1, wc,
-                                               kStatusTimeoutMma, &abort_flag, false));
+                ok = __all_sync(~0u, pa_wait_in(&bars.s_full[x][sl], (SLOTS == 2 ? ns >> 1 : ns) & 1, kStatusTimeoutMma, wc));
                 if (!ok) break;
                 if (w.nk < (kt + 1) * KEYS) {
                     // A part tile (the item's last): V's rows behind the sequence in
@@ -968,8 +986,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // same.)
                     const int idx = g + 2 * w.n - 1;
                     const int st = idx % G::STAGES, use = idx / G::STAGES;
-                    ok = __all_sync(~0u, mbar_wait(&bars.kv_full[st], use & 1, wc, kStatusTimeoutLoad,
-                                                   &abort_flag, false));
+                    ok = __all_sync(~0u, pa_wait_in(&bars.kv_full[st], use & 1, kStatusTimeoutLoad, wc));
                     if (!ok) break;
                     const int keys = max(w.nk - kt * KEYS, 0), end = max((keys + 15) / 16, 1) * 16;
                     const uint32_t dst = smem_u32(sKV) + st * G::TILE;

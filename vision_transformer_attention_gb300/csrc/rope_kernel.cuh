@@ -18,16 +18,19 @@
 //
 // Bound: every element is read and written once (memory). Two kernels:
 //
-//   rope_wide_kernel, where everything can move in 16-byte vectors. Persistent
-//   warps walk over (token, pass) items, a pass being 32 / L heads of one role:
-//   L lanes take a head, each lane two vectors. The vectors of the next
-//   kRopeStages - 1 passes are on their way into a shared-memory ring
-//   (cp.async, each lane reads back only what it asked for, so no barrier);
-//   with loads into registers a warp had one pass in flight and reached 2.4
-//   to 4.2 TB/s. A token's cosines and sines are formed once, by the lanes
-//   together, and stay in registers for all of its heads. A head's norm is a
-//   butterfly over its L lanes, and the arithmetic runs on pairs of floats
-//   (one instruction for two).
+//   Where everything can move in 16-byte vectors, persistent warps: L lanes take
+//   a head, each lane two vectors, 32 / L heads at a time (a pass). The vectors
+//   of the next kRopeStages - 1 passes are on their way into a shared-memory
+//   ring (cp.async, each lane reads back only what it asked for, so no barrier);
+//   with loads into registers a warp had one pass in flight and reached 2.4 to
+//   4.2 TB/s. Cosines and sines are formed once per token, by the lanes
+//   together. A head's norm is a butterfly over its L lanes, and the arithmetic
+//   runs on pairs of floats (one instruction for two).
+//     rope_token_kernel: a warp takes a token's passes, angles and gains in
+//     registers, addresses by additions.
+//     rope_run_kernel, for few heads: a warp takes a run of (token, head) rows
+//     whatever tokens they belong to, so that no lanes idle and a token's start
+//     is not paid per pass; angles and gains in shared memory.
 //
 //   rope_any_kernel, for every other stride, alignment and pair count: the
 //   same split, element by element, V at a time, no ring.
@@ -157,7 +160,7 @@ struct Wide<__half> {
 
 template <typename T, bool INTER, bool NORM>
 __global__ void __launch_bounds__(32 * kRopeWarps, rope_ctas_per_sm(NORM))
-rope_wide_kernel(const RopeArgs A) {
+rope_token_kernel(const __grid_constant__ RopeArgs A) {
     using W = Wide<T>;
     constexpr int E = W::E;  // elements per vector: a lane holds 2 E, E pairs
     extern __shared__ __align__(128) float rope_smem[];
@@ -380,7 +383,7 @@ rope_wide_kernel(const RopeArgs A) {
 }
 
 template <typename T>
-cudaError_t rope_launch_wide(RopeArgs A, cudaStream_t stream) {
+cudaError_t rope_launch_token(RopeArgs A, cudaStream_t stream) {
     constexpr int E = Wide<T>::E;
     const int slots = A.rotary / (2 * E) + (A.d - A.rotary + 2 * E - 1) / (2 * E);
     A.lanes = 1;
@@ -398,9 +401,269 @@ cudaError_t rope_launch_wide(RopeArgs A, cudaStream_t stream) {
                         static_cast<size_t>(kRopeWarps) * A.rotary * sizeof(float) +
                         (norm ? 2 * (A.d + E) * sizeof(float) : 0);
     void (*kernel)(const RopeArgs) =
-        A.interleaved ? (norm ? rope_wide_kernel<T, true, true> : rope_wide_kernel<T, true, false>)
-                      : (norm ? rope_wide_kernel<T, false, true> : rope_wide_kernel<T, false, false>);
+        A.interleaved ? (norm ? rope_token_kernel<T, true, true> : rope_token_kernel<T, true, false>)
+                      : (norm ? rope_token_kernel<T, false, true> : rope_token_kernel<T, false, false>);
     return launch_pdl(kernel, grid, dim3(32 * kRopeWarps), smem, stream, A);
+}
+
+template <typename T, bool INTER, bool NORM>
+__global__ void __launch_bounds__(32 * kRopeWarps, rope_ctas_per_sm(NORM))
+rope_run_kernel(const __grid_constant__ RopeArgs A) {
+    using W = Wide<T>;
+    constexpr int E = W::E;  // elements per vector: a lane holds 2 E, E pairs
+    extern __shared__ __align__(128) float rope_smem[];
+    const int pairs = A.rotary / 2, heads = A.heads[0] + A.heads[1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // shared memory: the ring [stage][vector][thread] of 16 bytes, the gains of
+    // both roles in fp32, each warp's cosines and sines [token][pair]
+    constexpr int kRingFloats = kRopeStages * 2 * 32 * kRopeWarps * 4;
+    float *gain_s = rope_smem + kRingFloats;
+    const int gain_row = A.d + E;  // E zeros behind each, for lanes without a second vector
+    float *cos_s = gain_s + (NORM ? 2 * gain_row : 0) + warp * 2 * A.run_tokens * pairs;
+    float *sin_s = cos_s + A.run_tokens * pairs;
+    const uint32_t ring = smem_u32(rope_smem) + threadIdx.x * 16;
+    constexpr uint32_t kVec = 32 * kRopeWarps * 16, kStage = 2 * kVec;
+
+    const int L = A.lanes, HP = 32 / L;
+    const int group = lane / L, sl = lane & (L - 1);
+    // This lane's slot: the element offsets of its two vectors. Slots below
+    // srot turn; the others hold two neighbouring vectors of the part that
+    // passes (the last of them may have one).
+    const int srot = A.rotary / (2 * E);
+    const bool rot = sl < srot;
+    const int o1 = rot && !INTER ? sl * E : (rot ? 2 * sl * E : A.rotary + 2 * (sl - srot) * E);
+    const int o2 = rot && !INTER ? pairs + sl * E : o1 + E;
+    const bool has1 = o1 < A.d, has2 = o2 < A.d;
+
+    const int64_t rows = A.units * heads, runs = (rows + A.run_rows - 1) / A.run_rows;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRopeWarps;
+    const int64_t run0 = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
+    const float inv_heads = 1.f / static_cast<float>(heads), inv_d = 1.f / static_cast<float>(A.d);
+
+    // A run: its first token and that token's batch and position, the rows of
+    // the token that lie before it, its length.
+    struct Run {
+        int64_t id, unit;
+        uint32_t b, t;
+        int skip, rows;
+    };
+    const auto enter = [&](Run &r, int64_t id) {
+        r.id = id;
+        if (id >= runs) return;
+        const int64_t row = id * A.run_rows;
+        r.unit = row / heads;
+        r.skip = static_cast<int>(row - r.unit * heads);
+        r.rows = static_cast<int>(rows - row < A.run_rows ? rows - row : A.run_rows);
+        r.b = A.units == A.tokens ? 0 : static_cast<uint32_t>(r.unit / A.tokens);
+        r.t = static_cast<uint32_t>(r.unit - r.b * A.tokens);
+    };
+    // Row i of the run: its token within the run, its role and its first channel.
+    // (The products of small numbers below cannot reach the next integer.)
+    const auto locate = [&](const Run &r, int i, const RopeView *views, int &tok, int &role) -> T * {
+        const int at = r.skip + i;
+        tok = static_cast<int>((static_cast<float>(at) + 0.5f) * inv_heads);
+        int h = at - tok * heads;
+        role = h >= A.heads[0] ? 1 : 0;
+        h -= role ? A.heads[0] : 0;
+        uint32_t b = r.b, t = r.t + tok;
+        while (t >= static_cast<uint32_t>(A.tokens)) {
+            t -= static_cast<uint32_t>(A.tokens);
+            ++b;
+        }
+        const RopeView &v = views[role];
+        return static_cast<T *>(v.data) + b * v.batch_stride + t * v.token_stride + h * v.head_stride;
+    };
+
+    griddep_wait();
+    if constexpr (NORM) {
+        for (int i = threadIdx.x; i < 2 * gain_row; i += 32 * kRopeWarps) {
+            const int role = i >= gain_row ? 1 : 0, e = i - role * gain_row;
+            const void *g = A.gain[role];
+            gain_s[i] = e >= A.d       ? 0.f
+                        : g == nullptr ? 1.f
+                                       : (A.gain_f32 ? static_cast<const float *>(g)[e]
+                                                     : to_f32(static_cast<const T *>(g)[e]));
+        }
+        __syncthreads();
+    }
+    if (run0 >= runs) return;
+
+    Run in, out;
+    enter(in, run0);
+    int in_row = group;  // of the run `in`, the next to be asked for
+    const auto ask = [&](int stage) {  // the next pass's vectors into the ring
+        if (in.id < runs) {
+            if (in_row < in.rows && has1) {
+                int tok, role;
+                const T *src = locate(in, in_row, A.src, tok, role);
+                cp_async16(ring + stage * kStage, src + o1);
+                if (has2) cp_async16(ring + stage * kStage + kVec, src + o2);
+            }
+            in_row += HP;
+            if (in_row - group >= in.rows) {
+                enter(in, in.id + stride);
+                in_row = group;
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kRopeStages - 1; ++s) ask(s);
+
+    const auto turn = [&](float2 v1, float2 v2, float2 c, float2 s, float2 &y1, float2 &y2) {
+        y1 = ffma2(v2, make_float2(-s.x, -s.y), fmul2(v1, c));
+        y2 = ffma2(v1, s, fmul2(v2, c));
+    };
+    int stage = 0;
+    for (int64_t id = run0; id < runs; id += stride) {
+        enter(out, id);
+        if (pairs > 0) {  // the angles of the run's tokens
+            const int tokens = static_cast<int>((static_cast<float>(out.skip + out.rows - 1) + 0.5f) * inv_heads) + 1;
+            __syncwarp();
+            for (int i = lane; i < tokens * pairs; i += 32) {
+                const int tok = i / pairs, p = i - tok * pairs;
+                uint32_t b = out.b, t = out.t + tok;
+                while (t >= static_cast<uint32_t>(A.tokens)) {
+                    t -= static_cast<uint32_t>(A.tokens);
+                    ++b;
+                }
+                const int64_t pos =
+                    A.positions[(b * A.pos_batch + t) * A.axes + (p < A.axis_pairs ? 0 : 1)];
+                const uint64_t angle = static_cast<uint64_t>(pos) * A.phases[p];
+                float sn, cs;
+                sincospif(static_cast<float>(static_cast<int32_t>(angle >> 32)) * 0x1p-31f, &sn, &cs);
+                cos_s[i] = cs * A.magnitude;
+                sin_s[i] = sn * (A.inverse ? -A.magnitude : A.magnitude);
+            }
+            __syncwarp();
+        }
+        for (int first = 0; first < out.rows; first += HP) {
+            const int i = first + group;
+            const bool live = i < out.rows && has1;
+            int tok = 0, role = 0;
+            T *dst = locate(out, live ? i : first, A.dst, tok, role);
+            float2 x[E / 2], y[E / 2];
+            cp_async_wait<kRopeStages - 2>();
+            {
+                uint4 a = make_uint4(0, 0, 0, 0), b = a;
+                if (live) a = ld_shared_v4(ring + stage * kStage);
+                if (live && has2) b = ld_shared_v4(ring + stage * kStage + kVec);
+                W::get(a, x);
+                W::get(b, y);
+            }
+            if constexpr (NORM) {
+                if (A.layer) {
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) sum = fadd2(sum, fadd2(x[e], y[e]));
+                    const float mean = lanes_sum(sum.x + sum.y, L) * inv_d;
+                    const float2 m1 = has1 ? make_float2(-mean, -mean) : make_float2(0.f, 0.f);
+                    const float2 m2 = has2 ? m1 : make_float2(0.f, 0.f);  // no channel, no mean
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        x[e] = fadd2(x[e], m1);
+                        y[e] = fadd2(y[e], m2);
+                    }
+                }
+                float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) sq = ffma2(x[e], x[e], ffma2(y[e], y[e], sq));
+                const float rs = rsqrtf(lanes_sum(sq.x + sq.y, L) * inv_d + A.eps);
+                const float2 rr = make_float2(rs, rs);
+                if (has1) {
+                    const float *g = gain_s + role * gain_row;
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        x[e] = fmul2(x[e], fmul2(rr, *reinterpret_cast<const float2 *>(g + o1 + 2 * e)));
+                        y[e] = fmul2(y[e], fmul2(rr, *reinterpret_cast<const float2 *>(g + o2 + 2 * e)));
+                    }
+                }
+            }
+            if (rot) {
+                const float *cp = cos_s + tok * pairs + sl * E, *sp = sin_s + tok * pairs + sl * E;
+                float2 c[E / 2], s[E / 2];
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    c[e] = *reinterpret_cast<const float2 *>(cp + 2 * e);
+                    s[e] = *reinterpret_cast<const float2 *>(sp + 2 * e);
+                }
+                if constexpr (INTER) {
+                    // pairs are neighbours: gather (x1, x1'), (x2, x2') and spread again
+#pragma unroll
+                    for (int e = 0; e < E / 4; ++e) {
+                        float2 u, v;
+                        turn(make_float2(x[2 * e].x, x[2 * e + 1].x),
+                             make_float2(x[2 * e].y, x[2 * e + 1].y), c[e], s[e], u, v);
+                        x[2 * e] = make_float2(u.x, v.x), x[2 * e + 1] = make_float2(u.y, v.y);
+                        turn(make_float2(y[2 * e].x, y[2 * e + 1].x),
+                             make_float2(y[2 * e].y, y[2 * e + 1].y), c[E / 4 + e], s[E / 4 + e], u, v);
+                        y[2 * e] = make_float2(u.x, v.x), y[2 * e + 1] = make_float2(u.y, v.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        float2 u, v;
+                        turn(x[e], y[e], c[e], s[e], u, v);
+                        x[e] = u, y[e] = v;
+                    }
+                }
+            }
+            if (live) {
+                *reinterpret_cast<uint4 *>(dst + o1) = W::put(x);
+                if (has2) *reinterpret_cast<uint4 *>(dst + o2) = W::put(y);
+            }
+            // the slot that this pass's predecessor was read from is free
+            ask(stage == 0 ? kRopeStages - 1 : stage - 1);
+            stage = stage + 1 == kRopeStages ? 0 : stage + 1;
+        }
+    }
+}
+
+template <typename T>
+cudaError_t rope_launch_run(RopeArgs A, cudaStream_t stream) {
+    constexpr int E = Wide<T>::E;
+    const int slots = A.rotary / (2 * E) + (A.d - A.rotary + 2 * E - 1) / (2 * E);
+    A.lanes = 1;
+    while (A.lanes < slots) A.lanes *= 2;
+    const bool norm = A.norm != 0;
+    const int HP = 32 / A.lanes, heads = A.heads[0] + A.heads[1], pairs = A.rotary / 2;
+    const int64_t rows = A.units * heads;
+    const int64_t most = static_cast<int64_t>(rope_ctas_per_sm(norm)) * sm_count();
+    // A run is as many passes as leave two runs per warp, 16 at most, and has no
+    // more tokens than 1024 pairs of angles (8 KB per warp) serve.
+    int64_t passes = rows / (2 * most * kRopeWarps * HP);
+    passes = passes < 1 ? 1 : passes > 16 ? 16 : passes;
+    const auto tokens_of = [&](int64_t p) { return static_cast<int>((p * HP + heads - 2) / heads + 1); };
+    while (passes > 1 && tokens_of(passes) * pairs > 1024) --passes;
+    A.run_rows = static_cast<int>(passes * HP);
+    A.run_tokens = tokens_of(passes);
+    const int64_t runs = (rows + A.run_rows - 1) / A.run_rows;
+    const int64_t ctas = (runs + kRopeWarps - 1) / kRopeWarps;
+    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
+    const size_t smem = kRopeStages * 2 * 32 * kRopeWarps * 16 +
+                        (norm ? 2 * (A.d + E) * sizeof(float) : 0) +
+                        static_cast<size_t>(kRopeWarps) * 2 * A.run_tokens * pairs * sizeof(float);
+    void (*kernel)(const RopeArgs) =
+        A.interleaved ? (norm ? rope_run_kernel<T, true, true> : rope_run_kernel<T, true, false>)
+                      : (norm ? rope_run_kernel<T, false, true> : rope_run_kernel<T, false, false>);
+    if (smem > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(smem));
+        if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(kernel, grid, dim3(32 * kRopeWarps), smem, stream, A);
+}
+
+// 16-byte vectors throughout: by token where its heads fill four passes or more
+// (40 heads of 128: 56 us by token, 70 in runs), else in runs (12 heads of 64: 32
+// and 24 us).
+template <typename T>
+cudaError_t rope_launch_wide(const RopeArgs &A, cudaStream_t stream) {
+    constexpr int E = Wide<T>::E;
+    const int slots = A.rotary / (2 * E) + (A.d - A.rotary + 2 * E - 1) / (2 * E);
+    return (A.heads[0] + A.heads[1]) * slots >= 4 * 32 ? rope_launch_token<T>(A, stream)
+                                                       : rope_launch_run<T>(A, stream);
 }
 
 template <typename T, int V, bool INTER, bool NORM>

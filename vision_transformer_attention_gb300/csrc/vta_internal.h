@@ -160,7 +160,9 @@ struct RopeArgs {
     int norm, layer, gain_f32;  // norm each head first; by its variance; gains in fp32
     const void *gain[2];        // [d], or NULL
     float eps;
-    int lanes, wpt;  // set by the launcher: lanes per head, warps per token
+    // set by the launchers: lanes per head; rows and most tokens of a run, or
+    // warps per token
+    int lanes, run_rows, run_tokens, wpt;
 };
 cudaError_t launch_rope_bf16(const RopeArgs &a, cudaStream_t stream);
 cudaError_t launch_rope_f16(const RopeArgs &a, cudaStream_t stream);
