@@ -60,6 +60,9 @@ static_assert(128 * kPaRegsControl + 256 * kPaRegsSoftmax <= kPaThreads * kPaReg
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 11;  // kWarpMma + tile
 enum { kWhole = 0, kShared = 1, kAlternate = 2 };
 constexpr int kWorkSlots = 3;
+// What starting an item costs beside its key tiles, in key tiles.
+template <int KIND>
+constexpr int kPaStart = KIND == kAlternate ? 1 : 2;
 constexpr float kPaMove = 256.f;  // a tile's sum that moves the reference
 // ... and one that has the tile done again: every p is below its tile's sum, so
 // p stays finite in the type, and its products and sums in fp32
@@ -355,24 +358,47 @@ __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRin
     }
 }
 
-// Units (key tiles of one item) and items of a sequence; an item is TT tokens
-// of one key/value head.
-template <int KEYS>
+// The CTAs' shares of `all` units: the first `more` CTAs have size + 1 units, the
+// others size. No more CTAs than units, so that an item's pieces lie on
+// neighbouring ones. Divisions in 32 bits where the numbers allow it (a division
+// in 64 bits takes some 500 cycles here, in front of everything else).
+struct PaShares {
+    int ctas, more;
+    long long size;
+    __device__ __forceinline__ PaShares(long long all, int grid) {
+        ctas = static_cast<int>(all < grid ? all : grid);
+        size = divide(all, ctas > 0 ? ctas : 1);
+        more = static_cast<int>(all - size * ctas);
+    }
+    static __device__ __forceinline__ long long divide(long long a, long long b) {
+        if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+        return a / b;
+    }
+    __device__ __forceinline__ long long begin(int cta) const { return size * cta + min(cta, more); }
+    __device__ __forceinline__ int cta_of(long long unit) const {
+        const long long split = (size + 1) * more;
+        return static_cast<int>(unit < split ? divide(unit, size + 1) : more + divide(unit - split, size));
+    }
+};
+
+// Units (key tiles of one item, and kPaStart before them) and items of a
+// sequence; an item is TT tokens of one key/value head.
+template <int KEYS, int START>
 __device__ __forceinline__ void pa_units(const PackedAttnArgs &P, const PaSeq &s, int TT,
                                          long long *units, int *items) {
     long long u = 0;
     const int nt = (s.nq + TT - 1) / TT;
     if (!P.causal || nt <= 1)
-        u = static_cast<long long>(nt) * (nt ? pa_tiles<KEYS>(P, s, s.nq - 1) : 0);
+        u = static_cast<long long>(nt) * (nt ? pa_tiles<KEYS>(P, s, s.nq - 1) + START : 0);
     else
-        for (int t = 0; t < nt; ++t) u += pa_tiles<KEYS>(P, s, min(s.nq, (t + 1) * TT) - 1);
+        for (int t = 0; t < nt; ++t) u += pa_tiles<KEYS>(P, s, min(s.nq, (t + 1) * TT) - 1) + START;
     *units = u * P.heads_kv;
     *items = nt * P.heads_kv;
 }
 
 // Shared and alternate: this CTA's share [u0, u1) of all units, in (sequence,
 // tokens, head, key tile) order. per: sequences per warp of the count before.
-template <int KEYS, int D>
+template <int KEYS, int D, int START>
 __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRing<D> ring, int lane,
                                                    int TT, const long long *warp_units,
                                                    const int *warp_tiles, int per) {
@@ -394,10 +420,9 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
         ring.put(none, lane);
         return;
     }
-    // no more CTAs than units, so that an item's pieces lie on neighbouring CTAs
-    const long long ctas = all < gridDim.x ? all : gridDim.x;
-    const long long u0 = blockIdx.x < ctas ? all * blockIdx.x / ctas : 0;
-    const long long u1 = blockIdx.x < ctas ? all * (blockIdx.x + 1) / ctas : 0;
+    const PaShares shares(all, gridDim.x);
+    const bool mine = blockIdx.x < shares.ctas;
+    const long long u0 = mine ? shares.begin(blockIdx.x) : 0, u1 = mine ? shares.begin(blockIdx.x + 1) : 0;
     // the sequence that holds unit u0
     long long base = 0;
     int item = 0, i = 0;
@@ -416,7 +441,7 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
             s = PaSeq{0, 0, 0, 0};
             if (b + lane < P.batch) {
                 s = pa_seq(P, b + lane, &bad);
-                pa_units<KEYS>(P, s, TT, &u, &n);
+                pa_units<KEYS, START>(P, s, TT, &u, &n);
             }
             const long long us = warp_scan(u, lane);
             const int ns = warp_scan(n, lane);
@@ -443,7 +468,7 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
     for (int t = 0; u < u1;) {
         const int last = min(s.nq, (t + 1) * TT) - 1;
         const int kt = pa_tiles<KEYS>(P, s, last);
-        const long long span = static_cast<long long>(kt) * P.heads_kv;
+        const long long span = static_cast<long long>(kt + START) * P.heads_kv;
         if (t * TT >= s.nq) {  // next sequence
             ++b;
             t = 0;
@@ -457,10 +482,12 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
             ++t;
             continue;
         }
-        const int h = static_cast<int>((u - base) / kt);
-        const long long first = base + static_cast<long long>(h) * kt;  // the item's first unit
-        const int lo = static_cast<int>(u - first);
-        const int n = static_cast<int>(u1 - u < kt - lo ? u1 - u : kt - lo);
+        const int h = static_cast<int>(PaShares::divide(u - base, kt + START));
+        // the unit of the item's first key tile; the key tiles of this share
+        const long long first = base + static_cast<long long>(h) * (kt + START) + START;
+        const int lo = static_cast<int>(u > first ? u - first : 0);
+        const int n = static_cast<int>(u1 - first < kt ? u1 - first : kt) - lo;
+        if (n <= 0) break;  // the share ends before it
         const int tok = t * TT;
         PaWork w;
         w.q_tok = s.q0 + tok;
@@ -485,7 +512,7 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
                 for (int i = lane; i < w.toks; i += 32) P.ws_item[w.q_tok + i] = item;
         }
         if (!ring.put(w, lane)) return;
-        u += n;
+        u = first + lo + n;
     }
     ring.put(none, lane);
 }
@@ -558,7 +585,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if constexpr (PIECES) {
                 long long u;
                 int n;
-                pa_units<KEYS>(P, s, TT, &u, &n);
+                pa_units<KEYS, kPaStart<KIND>>(P, s, TT, &u, &n);
                 units += u;
                 tiles += n;
             } else {
@@ -600,7 +627,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (warp == kWarpSched) {
             PaRing<D> ring{work, bars.w_full, bars.w_empty, wc};
             if constexpr (PIECES) {
-                pa_schedule_pieces<KEYS, D>(P, ring, lane, TT, warp_units, warp_tiles, per);
+                pa_schedule_pieces<KEYS, D, kPaStart<KIND>>(P, ring, lane, TT, warp_units, warp_tiles, per);
             } else {
                 int most = 1;
                 for (int i = 0; i < kPaThreads / 32; ++i) most = max(most, warp_tiles[i]);
@@ -1142,9 +1169,8 @@ packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int grid) {
     const int tok = static_cast<int>(token - a.w), x = tok >= P.tile_tokens ? 1 : 0;
     const int row = (tok - x * P.tile_tokens) * P.group + (out_head - kv_head * P.group);
     const long long first = (static_cast<long long>(a.y) << 32) | static_cast<uint32_t>(a.x);
-    const long long ctas = all < grid ? all : grid;
-    const int c0 = static_cast<int>(((first + 1) * ctas - 1) / all);
-    const int c1 = static_cast<int>(((first + a.z) * ctas - 1) / all);
+    const PaShares shares(all, grid);
+    const int c0 = shares.cta_of(first), c1 = shares.cta_of(first + a.z - 1);
     const int pieces = (ALT ? 2 : 1) * (c1 - c0 + 1);
     const auto at = [&](int p) {
         return (static_cast<int64_t>(item + c0) * 2 + (ALT ? p : 2 * p + x)) * P.ws_rows + row;
