@@ -41,7 +41,7 @@ Plan make_plan(int64_t total_q, int64_t total_k, int batch, int heads_q, int hea
     p.ws_rows = static_cast<int>(least(128, group * least(p.tile_tokens, total_q)));
     const int D = d <= 64 ? 64 : 128;
     const size_t rows = static_cast<size_t>(p.max_items + p.ctas) * 2 * p.ws_rows;
-    p.item_at = 64 + static_cast<size_t>(p.max_items) * 32;
+    p.item_at = 64 + static_cast<size_t>(p.max_items) * 16;
     p.ml_at = (p.item_at + static_cast<size_t>(total_q) * sizeof(int32_t) + 127) & ~static_cast<size_t>(127);
     p.o_at = (p.ml_at + rows * sizeof(float2) + 127) & ~static_cast<size_t>(127);
     p.bytes = p.o_at + rows * D * sizeof(float);

@@ -411,10 +411,8 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
     PaWork none{};
     none.head = -1;
     int *header = static_cast<int *>(P.workspace);
-    if (blockIdx.x == 0 && lane == 0) {
-        *reinterpret_cast<long long *>(header) = all;
-        header[2] = tiles_all <= P.max_items ? tiles_all : 0;
-    }
+    if (blockIdx.x == 0 && lane == 0)
+        header[0] = tiles_all <= P.max_items ? tiles_all : 0;
     if (tiles_all > P.max_items) {  // overlapping sequences: the workspace is too small
         if (lane == 0) atomicOr(P.status, kStatusBadSequence);
         ring.put(none, lane);
@@ -504,9 +502,8 @@ __device__ __forceinline__ void pa_schedule_pieces(const PackedAttnArgs &P, PaRi
         w.slot = item + h + blockIdx.x;
         if (lo == 0) {  // for the kernel that joins the pieces: the item, and its tokens' item
             if (lane == 0) {
-                meta[2 * (item + h)] = make_int4(static_cast<int>(first & 0xFFFFFFFFll),
-                                                 static_cast<int>(first >> 32), kt, w.q_tok);
-                meta[2 * (item + h) + 1] = make_int4(w.toks, h, 0, 0);
+                const int ctas = n == kt ? 1 : shares.cta_of(first + kt - 1) - static_cast<int>(blockIdx.x) + 1;
+                meta[item + h] = make_int4(blockIdx.x, ctas | h << 16, w.q_tok, w.toks);
             }
             if (h == 0)
                 for (int i = lane; i < w.toks; i += 32) P.ws_item[w.q_tok + i] = item;
@@ -1141,96 +1138,138 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 }
 
 // Joins the pieces of the rows: out = sum_p 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p.
-// WIDE: a CTA per row, its warps taking every eighth piece (few rows, many
-// pieces); otherwise a warp per row. Rows of no sequence are left alone: their
-// entry of ws_item is whatever the workspace held, which is believed only if the
-// item it names says that it holds the row.
+// Its time is that of its chain of reads (the row's item, the item's pieces,
+// then (m, l) and O together), so nothing is divided between them, the first O
+// vectors are under way before their factors are known, and half a warp takes a
+// row where rows are many. WIDE: a CTA per row, its warps taking every eighth
+// piece (few rows, many pieces). Rows of no sequence are left alone: their entry
+// of ws_item is whatever the workspace held, which is believed only if the item
+// it names says that it holds the row.
 constexpr int kJoinWarps = 8;
+
+template <int N>
+__device__ __forceinline__ float join_max(float v) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+
+template <int N>
+__device__ __forceinline__ float join_sum(float v) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
 
 template <typename T, int D, bool ALT, bool WIDE>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int grid) {
-    constexpr int C = D / 32;  // columns per lane
+packed_combine_kernel(const __grid_constant__ PackedAttnArgs P) {
+    constexpr int LANES = WIDE ? 32 : 16;             // of a row
+    constexpr int W = D / LANES < 4 ? D / LANES : 4;  // floats of a vector
+    constexpr int N = D / LANES / W;                  // vectors of a lane, LANES * W apart
+    constexpr int STEP = WIDE ? kJoinWarps : 1, U = 4;
     __shared__ float part[WIDE ? kJoinWarps : 1][WIDE ? D : 1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t out_row = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
-    const int heads = P.group * P.heads_kv;
-    const int64_t token = out_row / heads;
-    if (token >= P.total_q) return;
-    const int out_head = static_cast<int>(out_row - token * heads), kv_head = out_head / P.group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LANES - 1);
+    const int heads = P.group * P.heads_kv, rows = P.total_q * heads;  // below 2^31
+    const int want = WIDE ? blockIdx.x : blockIdx.x * (2 * kJoinWarps) + threadIdx.x / LANES;
+    const int out_row = min(want, rows - 1);
+    const int token = out_row / heads;
+    const int out_head = out_row - token * heads, kv_head = out_head / P.group;
     griddep_wait();
     const int *header = static_cast<const int *>(P.workspace);
-    const long long all = *reinterpret_cast<const long long *>(header);
-    const int count = header[2], item = P.ws_item[token] + kv_head;
-    if (item < kv_head || item >= count) return;
-    const int4 *meta = reinterpret_cast<const int4 *>(header + 16) + 2 * item;
-    const int4 a = meta[0], b = meta[1];
-    if (token < a.w || token >= a.w + b.x || b.y != kv_head) return;
-    const int tok = static_cast<int>(token - a.w), x = tok >= P.tile_tokens ? 1 : 0;
+    const int count = header[0], item = P.ws_item[token] + kv_head;
+    bool valid = want < rows && item >= kv_head && item < count;
+    const int4 a = valid ? reinterpret_cast<const int4 *>(header + 16)[item] : make_int4(0, 0, 0, 0);
+    const int tok = token - a.z, x = tok >= P.tile_tokens ? 1 : 0;
+    valid = valid && tok >= 0 && tok < a.w && static_cast<int>(static_cast<uint32_t>(a.y) >> 16) == kv_head;
     const int row = (tok - x * P.tile_tokens) * P.group + (out_head - kv_head * P.group);
-    const long long first = (static_cast<long long>(a.y) << 32) | static_cast<uint32_t>(a.x);
-    const PaShares shares(all, grid);
-    const int c0 = shares.cta_of(first), c1 = shares.cta_of(first + a.z - 1);
-    const int pieces = (ALT ? 2 : 1) * (c1 - c0 + 1);
-    const auto at = [&](int p) {
-        return (static_cast<int64_t>(item + c0) * 2 + (ALT ? p : 2 * p + x)) * P.ws_rows + row;
+    const int pieces = valid ? (ALT ? 2 : 1) * (a.y & 0xFFFF) : 0;
+    const int64_t at0 = (static_cast<int64_t>(item + a.x) * 2 + (ALT ? 0 : x)) * P.ws_rows + row;
+    const int64_t hop = static_cast<int64_t>(ALT ? 1 : 2) * P.ws_rows;
+    const int most = WIDE ? pieces : max(pieces, __shfl_xor_sync(~0u, pieces, 16));
+
+    float M = -INFINITY, L = 0.f, acc[N][W], v[U][N][W];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < W; ++e) acc[n][e] = 0.f;
+    const auto fetch = [&](int p) {  // O of pieces p, p + STEP, ...
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (p + u * STEP < pieces)
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const float *src = P.ws_o + (at0 + (p + u * STEP) * hop) * D + (n * LANES + lane) * W;
+                    if constexpr (W == 4)
+                        *reinterpret_cast<float4 *>(v[u][n]) = *reinterpret_cast<const float4 *>(src);
+                    else
+                        *reinterpret_cast<float2 *>(v[u][n]) = *reinterpret_cast<const float2 *>(src);
+                }
     };
-    float M = -INFINITY;
-    for (int p = lane; p < pieces; p += 32) M = fmaxf(M, P.ws_ml[at(p)].x);
+    for (int p0 = 0; p0 < most; p0 += LANES) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (p0 + lane < pieces) ml = P.ws_ml[at0 + (p0 + lane) * hop];
+        int q = WIDE ? warp : 0;
+        fetch(p0 + q);
+        const float top = fmaxf(M, join_max<LANES>(ml.y == 0.f ? -INFINITY : ml.x));
+        const float base = top == -INFINITY ? 0.f : top;
+        const float keep = M == -INFINITY ? 0.f : ex2_approx(M - base);
+        // no key seen: nothing was written
+        const float f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - base);
+        L = L * keep + join_sum<LANES>(f * ml.y);
+        M = top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    for (int p = lane; p < pieces; p += 32) {
-        const float2 ml = P.ws_ml[at(p)];
-        if (ml.y != 0.f) L += ml.y * ex2_approx(ml.x - base);
-    }
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
-    float acc[C];
+            for (int e = 0; e < W; ++e) acc[n][e] *= keep;
+        for (; q < LANES && p0 + q < most; q += U * STEP) {
+            if (q >= U * STEP) fetch(p0 + q);
 #pragma unroll
-    for (int e = 0; e < C; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int p = WIDE ? warp : 0; p < pieces; p += WIDE ? kJoinWarps : 1) {
-        const int64_t i = at(p);
-        const float2 ml = P.ws_ml[i];
-        if (ml.y == 0.f) continue;  // no key seen: nothing was written
-        const float f = ex2_approx(ml.x - base);
-        const float *src = P.ws_o + i * D + lane * C;
-        if constexpr (C == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(src);
-            acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(src);
-            acc[0] += f * v.x, acc[1] += f * v.y;
+            for (int u = 0; u < U; ++u) {
+                const float fu = __shfl_sync(~0u, f, (q + u * STEP) & (LANES - 1), LANES);
+                if (fu != 0.f && p0 + q + u * STEP < pieces && q + u * STEP < LANES)
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+#pragma unroll
+                        for (int e = 0; e < W; ++e) acc[n][e] += fu * v[u][n][e];
+            }
         }
     }
     if constexpr (WIDE) {
 #pragma unroll
-        for (int e = 0; e < C; ++e) part[warp][lane * C + e] = acc[e];
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < W; ++e) part[warp][(n * LANES + lane) * W + e] = acc[n][e];
         __syncthreads();
         if (warp != 0) return;
 #pragma unroll
-        for (int e = 0; e < C; ++e) {
-            float s = 0.f;
+        for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int i = 0; i < kJoinWarps; ++i) s += part[i][lane * C + e];
-            acc[e] = s;
-        }
+            for (int e = 0; e < W; ++e) {
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < kJoinWarps; ++i) s += part[i][(n * LANES + lane) * W + e];
+                acc[n][e] = s;
+            }
     }
+    if (!valid) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     if (lane == 0 && P.lse != nullptr)
         P.lse[out_row] =
             L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
-    if (lane * C >= P.d) return;
-    T *dst = static_cast<T *>(P.out) + token * P.out_token + out_head * P.out_head + lane * C;
+    T *dst = static_cast<T *>(P.out) + token * P.out_token + out_head * P.out_head;
 #pragma unroll
-    for (int e = 0; e < C; ++e) acc[e] = L == 0.f ? 0.f : acc[e] * inv;
-    if constexpr (C == 4)
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pa_pack<T>(acc[0], acc[1]), pa_pack<T>(acc[2], acc[3]));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = pa_pack<T>(acc[0], acc[1]);
+    for (int n = 0; n < N; ++n) {
+        const int col = (n * LANES + lane) * W;
+        if (col >= P.d) continue;
+        float *o = acc[n];
+#pragma unroll
+        for (int e = 0; e < W; ++e) o[e] = L == 0.f ? 0.f : o[e] * inv;
+        if constexpr (W == 4)
+            *reinterpret_cast<uint2 *>(dst + col) = make_uint2(pa_pack<T>(o[0], o[1]), pa_pack<T>(o[2], o[3]));
+        else
+            *reinterpret_cast<uint32_t *>(dst + col) = pa_pack<T>(o[0], o[1]);
+    }
 }
 
 template <typename T, int D, int KIND>
@@ -1248,10 +1287,10 @@ cudaError_t pa_launch_kind(const PackedAttnMaps &m, const PackedAttnArgs &a, int
         const int64_t rows = static_cast<int64_t>(a.total_q) * a.group * a.heads_kv;
         if (rows <= 4 * sm_count())
             return launch_pdl(packed_combine_kernel<T, D, ALT, true>, dim3(static_cast<unsigned>(rows)),
-                              dim3(32 * kJoinWarps), 0, stream, a, ctas);
+                              dim3(32 * kJoinWarps), 0, stream, a);
         return launch_pdl(packed_combine_kernel<T, D, ALT, false>,
-                          dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps)),
-                          dim3(32 * kJoinWarps), 0, stream, a, ctas);
+                          dim3(static_cast<unsigned>((rows + 2 * kJoinWarps - 1) / (2 * kJoinWarps))),
+                          dim3(32 * kJoinWarps), 0, stream, a);
     }
     return err;
 }
