@@ -947,7 +947,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     const unsigned rows_ok = __ballot_sync(~0u, due.valid) >> (lane & ~3);
                     constexpr int COLS = PIECES ? 16 : 32;  // 64 bytes
 #pragma unroll 1
-                    for (int q = 0; q < D; q += COLS) {
+                    for (int q = 0; q < P.d; q += COLS) {
                         uint32_t v[16];
                         if (due.live) {
                             if constexpr (PIECES) {
@@ -965,7 +965,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                                                  __uint_as_float(o[2 * e + 1]) * inv);
                             }
                         }
-                        if (q == D - COLS) {
+                        if (q + COLS >= P.d) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&bars.o_empty[x]);
