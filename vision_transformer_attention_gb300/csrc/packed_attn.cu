@@ -124,7 +124,7 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     const Plan p = make_plan(total_q, total_k, batch, heads_q, heads_kv, d);
     if (p.bytes > 0 && (workspace == nullptr || !aligned(workspace, 128) || workspace_bytes < p.bytes))
         return RPE_ERR_INVALID_ARG;
-    if (p.kind && (p.max_items > INT32_MAX / 2 || total_q * heads_q > INT32_MAX))
+    if (p.kind && (p.max_items > INT32_MAX / 2 || total_q * heads_q > INT32_MAX - 64))
         return RPE_ERR_UNSUPPORTED;
 
     PackedAttnArgs a{};
