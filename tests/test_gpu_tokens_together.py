@@ -289,3 +289,15 @@ def test_batches_of_few_tokens_and_few_heads(batch, tokens, hq, hk, d):
             if src is not None:
                 check_rope(normed, ref_rope(src, at, freqs, 1, norm=_lib.RPE_NORM_RMS))
                 check_rope(turned, ref_rope(src, at, freqs, 1))
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_no_keys_no_queries_no_sequences(causal):
+    q, none = _randn(5, 4, 64, seed=97), torch.empty(0, 2, 64, dtype=BF16, device="cuda")
+    out, lse = api.packed_attn_fwd(q, none, none, _cu([2, 3]), _ints([0, 0, 0]), causal=causal,
+                                   return_lse=True)
+    assert not bool(out.any()) and bool((lse == -float("inf")).all())
+    assert api.packed_attn_fwd(q[:0], q[:, :2], q[:, :2], _cu([0]), _cu([5])).shape == (0, 4, 64)
+    kept = torch.full_like(q, 2.0)
+    api.packed_attn_fwd(q, q, q, _ints([0]), out=kept)
+    assert bool((kept == 2).all())

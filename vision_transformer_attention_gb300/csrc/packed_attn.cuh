@@ -11,21 +11,30 @@
 // on two such tiles at a time, each with its own softmax warpgroup, one thread
 // per row, and its own issuing thread for the tensor-core products, so that one
 // tile's softmax and waits run under the other's products (with one issuing
-// thread for both the tensor pipe stood still during its waits: 1.08 instead of
-// XXXX PFLOP/s on long causal prompts). Three kinds of work:
+// thread for both the tensor pipe stood still during its waits: 501 us on long
+// causal prompts, 487 with two, when the rest was as slow as then).
+//
+// Measured (device time): causal prompts of 500 to 8192 tokens, 32 over 8 heads
+// of 128, 385 us, 1520 TFLOP/s, 1700 once items are long, where the tensor pipe
+// waits for little but the softmax's exponentials; images of 196 to 3136
+// patches, 6 heads of 64, 191 us, 870 TFLOP/s (half the product per
+// exponential); a token each against 32 caches of 110 to 7927 keys, 52 us,
+// 4.9 TB/s (6.4 with 7680 keys each: 17 us of start, end and join).
+//
+// Three kinds of work:
 //   whole (kWhole): two neighbouring tiles of one sequence and key/value head,
 //     sharing every key tile, all keys;
 //   shared (kShared; too few items to fill the GPU): the same against a run of
 //     the key tiles;
 //   alternate (kAlternate; rows for one tile at most): one tile against a run
 //     of key tiles, the warpgroups taking every other key tile of it.
-// In the last two a CTA's runs are its equal share of all key tiles, the
-// unnormalised outputs go to the caller's workspace in fp32, and
-// packed_combine_kernel joins them.
+// In the last two a CTA's runs are its equal share of all key tiles (and of
+// what starting an item costs), the unnormalised outputs go to the caller's
+// workspace in fp32, and packed_combine_kernel joins them.
 //
-// Per key tile (128 keys, or 96 for D = 64) and tile: S = Q K^T into tensor memory (fp32), the row's 128
-// scores into registers, the running maximum, p = 2^(scale log2e (s - m)) in
-// fp32, summed in fp32 and rounded to the 16-bit type over the scores, where
+// Per key tile (128 keys, or 96 for D = 64) and tile: S = Q K^T into tensor
+// memory (fp32), the row's scores into registers, p = 2^(scale log2e (s - m))
+// in fp32, summed in fp32 and rounded to the 16-bit type over the scores, where
 // the product P V reads its A operand, at most half a step off (2^-8 for bf16,
 // 2^-11 for fp16 of itself), the precision that the values have. The reference
 // m is the row's maximum over its first key tile; later tiles form no maximum
@@ -61,6 +70,8 @@ constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 11;  // kWarpMma + tile
 enum { kWhole = 0, kShared = 1, kAlternate = 2 };
 constexpr int kWorkSlots = 3;
 // What starting an item costs beside its key tiles, in key tiles.
+// Single tokens against 32 caches of 110 to 7927 keys: 66 us with nothing for
+// it, 55 with one, 56 with two or three; a prompt's piece 92, 92 (two), 93 (six).
 template <int KIND>
 constexpr int kPaStart = KIND == kAlternate ? 1 : 2;
 constexpr float kPaMove = 256.f;  // a tile's sum that moves the reference
@@ -1163,7 +1174,7 @@ __device__ __forceinline__ float join_sum(float v) {
 
 template <typename T, int D, bool ALT, bool WIDE>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-packed_combine_kernel(const __grid_constant__ PackedAttnArgs P) {
+packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int ctas) {
     constexpr int LANES = WIDE ? 32 : 16;             // of a row
     constexpr int W = D / LANES < 4 ? D / LANES : 4;  // floats of a vector
     constexpr int N = D / LANES / W;                  // vectors of a lane, LANES * W apart
@@ -1183,6 +1194,8 @@ packed_combine_kernel(const __grid_constant__ PackedAttnArgs P) {
     const int tok = token - a.z, x = tok >= P.tile_tokens ? 1 : 0;
     valid = valid && tok >= 0 && tok < a.w && static_cast<int>(static_cast<uint32_t>(a.y) >> 16) == kv_head;
     const int row = (tok - x * P.tile_tokens) * P.group + (out_head - kv_head * P.group);
+    // (in range whatever the entry holds: after a wait that ran out it may be stale)
+    valid = valid && row >= 0 && row < P.ws_rows && a.x >= 0 && a.x + (a.y & 0xFFFF) <= ctas;
     const int pieces = valid ? (ALT ? 2 : 1) * (a.y & 0xFFFF) : 0;
     const int64_t at0 = (static_cast<int64_t>(item + a.x) * 2 + (ALT ? 0 : x)) * P.ws_rows + row;
     const int64_t hop = static_cast<int64_t>(ALT ? 1 : 2) * P.ws_rows;
@@ -1287,10 +1300,10 @@ cudaError_t pa_launch_kind(const PackedAttnMaps &m, const PackedAttnArgs &a, int
         const int64_t rows = static_cast<int64_t>(a.total_q) * a.group * a.heads_kv;
         if (rows <= 4 * sm_count())
             return launch_pdl(packed_combine_kernel<T, D, ALT, true>, dim3(static_cast<unsigned>(rows)),
-                              dim3(32 * kJoinWarps), 0, stream, a);
+                              dim3(32 * kJoinWarps), 0, stream, a, ctas);
         return launch_pdl(packed_combine_kernel<T, D, ALT, false>,
                           dim3(static_cast<unsigned>((rows + 2 * kJoinWarps - 1) / (2 * kJoinWarps))),
-                          dim3(32 * kJoinWarps), 0, stream, a);
+                          dim3(32 * kJoinWarps), 0, stream, a, ctas);
     }
     return err;
 }
