@@ -301,3 +301,19 @@ def test_no_keys_no_queries_no_sequences(causal):
     kept = torch.full_like(q, 2.0)
     api.packed_attn_fwd(q, q, q, _ints([0]), out=kept)
     assert bool((kept == 2).all())
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("hq,hkv,d,dtype", [(6, 3, 80, BF16), (4, 4, 64, F16), (4, 2, 128, BF16),
+                                            (5, 5, 24, BF16), (8, 1, 128, F16)])
+def test_short_sequences(hq, hkv, d, dtype, causal):
+    # two heads of a sequence at once, an odd head left over, long sequences and empty ones among
+    # them, keys of one tile and more, none at all, NaN behind the keys
+    rng = random.Random(hq * d)
+    tile = 128 * hkv // hq
+    sizes = [0, 1, 2, tile // 3, tile // 2, tile - 1, tile]
+    nq = [rng.choice(sizes) for _ in range(400)]
+    nq[7], nq[300], nq[301] = tile + 1, 5 * tile + 3, 2 * tile
+    _run(nq, nq, hq, hkv, d, causal, dtype, seed=200)
+    nk = [rng.choice([0, 1, 40, 95, 96, 97, 128, 129, 200]) for _ in nq]
+    _run(nq, nk, hq, hkv, d, causal, dtype, seed=201, capacity=210)

@@ -13,7 +13,7 @@ namespace {
 
 // How a call is split, from sizes that the host knows.
 struct Plan {
-    int kind;  // 0 whole items, 1 pieces of two tiles, 2 pieces of one
+    int kind;  // 0 whole items, 1 pieces of two tiles, 2 pieces of one, 3 whole items, short ones by two heads
     int ctas, tile_tokens, ws_rows;
     int64_t max_items;
     size_t item_at, ml_at, o_at, bytes;  // workspace offsets and size (pieces)
@@ -34,9 +34,15 @@ Plan make_plan(int64_t total_q, int64_t total_k, int batch, int heads_q, int hea
     // to share out.
     const bool thin = total_q <= static_cast<int64_t>(batch) * p.tile_tokens / 2 && total_k >= 4 * total_q;
     const bool few = pairs < 2 * sms && total_k >= 512 * static_cast<int64_t>(batch);
-    p.kind = thin ? 2 : few ? 1 : 0;
-    p.ctas = static_cast<int>(p.kind ? sms : least(pairs, sms));
-    if (!p.kind) return p;
+    // Two heads of a short sequence at once where sequences have a tile and a half
+    // at most on average (one tile each: 41 us instead of 65; two each: 73 instead
+    // of 69) and the items are more than one round of the SMs.
+    const bool brief = heads_kv > 1 && 2 * total_q <= 3 * static_cast<int64_t>(batch) * p.tile_tokens &&
+                       pairs >= 2 * sms;
+    p.kind = thin ? 2 : few ? 1 : brief ? 3 : 0;
+    const bool pieces = p.kind == 1 || p.kind == 2;
+    p.ctas = static_cast<int>(pieces ? sms : least(pairs, sms));
+    if (!pieces) return p;
     p.max_items = thin ? ones : pairs;
     p.ws_rows = static_cast<int>(least(128, group * least(p.tile_tokens, total_q)));
     const int D = d <= 64 ? 64 : 128;
@@ -124,7 +130,7 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     const Plan p = make_plan(total_q, total_k, batch, heads_q, heads_kv, d);
     if (p.bytes > 0 && (workspace == nullptr || !aligned(workspace, 128) || workspace_bytes < p.bytes))
         return RPE_ERR_INVALID_ARG;
-    if (p.kind && (p.max_items > INT32_MAX / 2 || total_q * heads_q > INT32_MAX - 64))
+    if (p.bytes > 0 && (p.max_items > INT32_MAX / 2 || total_q * heads_q > INT32_MAX - 64))
         return RPE_ERR_UNSUPPORTED;
 
     PackedAttnArgs a{};
@@ -144,7 +150,7 @@ int packed_attn_fwd(const rpe_view *q, const rpe_view *k, const rpe_view *v, con
     a.out_token = total_q > 1 ? out->token_stride : 0;
     a.out_head = heads_q > 1 ? out->head_stride : 0;
     a.lse = lse;
-    if (p.kind) {
+    if (p.bytes > 0) {
         char *ws = static_cast<char *>(workspace);
         a.workspace = ws;
         a.ws_item = reinterpret_cast<int32_t *>(ws + p.item_at);

@@ -26,9 +26,14 @@
 //     sharing every key tile, all keys;
 //   shared (kShared; too few items to fill the GPU): the same against a run of
 //     the key tiles;
+//   twins (kTwins; sequences of one or two tiles on average): as whole, but a
+//     last item of one tile and one key tile takes two heads, a tile each, whose
+//     chains (load, S, softmax, P V, rows out: 3.9 us) then run side by side.
+//     (Sequences of 40 tokens, 12 over 4 heads of 80: 41 us, 65 as whole. In one
+//     kernel with the long ones it cost those: images 215 us, 191 without.)
 //   alternate (kAlternate; rows for one tile at most): one tile against a run
 //     of key tiles, the warpgroups taking every other key tile of it.
-// In the last two a CTA's runs are its equal share of all key tiles (and of
+// In shared and alternate a CTA's runs are its equal share of all key tiles (and of
 // what starting an item costs), the unnormalised outputs go to the caller's
 // workspace in fp32, and packed_combine_kernel joins them.
 //
@@ -67,7 +72,7 @@ constexpr int kPaThreads = 384;  // two softmax warpgroups, then loads, products
 constexpr int kPaRegsControl = 80, kPaRegsSoftmax = 208, kPaRegsLaunch = 168;
 static_assert(128 * kPaRegsControl + 256 * kPaRegsSoftmax <= kPaThreads * kPaRegsLaunch, "register split");
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpSched = 11;  // kWarpMma + tile
-enum { kWhole = 0, kShared = 1, kAlternate = 2 };
+enum { kWhole = 0, kShared = 1, kAlternate = 2, kTwins = 3 };
 constexpr int kWorkSlots = 3;
 // What starting an item costs beside its key tiles, in key tiles.
 // Single tokens against 32 caches of 110 to 7927 keys: 66 us with nothing for
@@ -126,6 +131,7 @@ struct PaWork {
     int lim0;   // keys that the first token sees (causal; may be <= 0)
     int lo, n;  // key tiles lo .. lo + n - 1
     int n0, n1; // of them, how many the two tiles need (alternate: not used)
+    int twin;   // twins: 1: tile x is the same tokens of head + x, its key tile the ring's x-th
     int slot;   // shared, alternate: where the unnormalised output goes
 };
 
@@ -299,7 +305,7 @@ struct PaRing {
 
 // Whole items, the costliest first (by key tiles, in at most 64 levels), dealt
 // to the CTAs round by round, every other round backwards.
-template <int KEYS, int D>
+template <int KEYS, int D, bool TWINS>
 __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRing<D> ring, int lane,
                                                   int most_tiles) {
     const int TT = 2 * P.tile_tokens;
@@ -332,13 +338,27 @@ __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRin
                 if (b0 + lane < P.batch) s = pa_seq(P, b0 + lane, &bad);
             }
             const int high = upto(s, q), mine = high - upto(s, q - 1);
-            const long long sum = warp_scan(static_cast<long long>(mine) * P.heads_kv, lane);
+            // a last item of one tile and one key tile takes its heads by twos
+            const bool single = TWINS && mine > 0 && s.nk <= KEYS &&
+                                s.nq - (s.nq - 1) / TT * TT <= P.tile_tokens;
+            const long long count = static_cast<long long>(mine) * P.heads_kv - (single ? P.heads_kv / 2 : 0);
+            const long long sum = warp_scan(count, lane);
             const long long all = __shfl_sync(~0u, sum, 31);
             while (alive && want < base + all) {
                 const uint32_t after = __ballot_sync(~0u, base + sum > want);
                 const int src = __ffs(after) - 1;
-                const long long first = base + sum - static_cast<long long>(mine) * P.heads_kv;
-                const int r = static_cast<int>(want - __shfl_sync(~0u, first, src));
+                const long long first = base + sum - count;
+                int r = static_cast<int>(want - __shfl_sync(~0u, first, src));
+                const bool by_twos = __shfl_sync(~0u, single ? 1 : 0, src) != 0;
+                int twin = 0;
+                if (by_twos) {
+                    if (2 * r < P.heads_kv) {
+                        r *= 2;
+                        twin = r + 1 < P.heads_kv ? 1 : 0;
+                    } else {
+                        r += P.heads_kv / 2;  // as if the last item had come head by head
+                    }
+                }
                 PaSeq q_seq{__shfl_sync(~0u, s.q0, src), __shfl_sync(~0u, s.nq, src),
                             __shfl_sync(~0u, s.k0, src), __shfl_sync(~0u, s.nk, src)};
                 const int t = __shfl_sync(~0u, high, src) - 1 - r / P.heads_kv;
@@ -355,6 +375,10 @@ __device__ __forceinline__ void pa_schedule_items(const PackedAttnArgs &P, PaRin
                 w.n1 = w.toks > P.tile_tokens ? pa_tiles<KEYS>(P, q_seq, min(q_seq.nq, tok + TT) - 1) : 0;
                 w.n = max(w.n0, w.n1);
                 w.slot = 0;
+                if (TWINS) {
+                    w.twin = twin;
+                    if (twin) w.n = 2, w.n1 = 1;
+                }
                 alive = ring.put(w, lane);
                 ++round;
                 want = target();
@@ -532,7 +556,8 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PackedAttnArgs P) {
     using G = PaGeo<D>;
-    constexpr bool ALT = KIND == kAlternate, PIECES = KIND != kWhole;
+    constexpr bool ALT = KIND == kAlternate, PIECES = KIND == kShared || KIND == kAlternate;
+    constexpr bool TWINS = KIND == kTwins;
     constexpr int KEYS = G::KEYS, SLOTS = ALT ? 1 : G::SLOTS;
     extern __shared__ __align__(1024) uint8_t pa_smem[];
     __shared__ PaBars bars;
@@ -639,7 +664,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             } else {
                 int most = 1;
                 for (int i = 0; i < kPaThreads / 32; ++i) most = max(most, warp_tiles[i]);
-                pa_schedule_items<KEYS, D>(P, ring, lane, most);
+                pa_schedule_items<KEYS, D, TWINS>(P, ring, lane, most);
             }
         } else if (warp == kWarpLoad) {
             if (lane == 0) {
@@ -651,7 +676,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             bool ok = true;
             const uint32_t q_bytes = 128u * P.group * P.tile_tokens * G::SLABS;
             PaWork w;
-            const auto load_q = [&](int i, int tok) {  // into buffer i
+            const auto load_q = [&](int i, int tok, int head) {  // into buffer i
                 ok = __all_sync(~0u, pa_wait<D>(&bars.q_empty[i], (q_loads[i] & 1) ^ 1, kStatusTimeoutSync, wc));
                 if (!ok) return;
                 ++q_loads[i];
@@ -659,17 +684,18 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mbar_arrive_expect_tx(&bars.q_full[i], q_bytes);
                     for (int sl = 0; sl < G::SLABS; ++sl)
                         tma_load_3d(sQ + i * G::Q_TILE + sl * kSlab, &tm_q, &bars.q_full[i], sl * 64,
-                                    w.head * P.group, w.q_tok + tok);
+                                    head * P.group, w.q_tok + tok);
                 }
             };
             int it = 0;
             while (ok && next_work(w)) {
+                const int twin = TWINS ? w.twin : 0;
                 const int tiles_q = ALT ? 1 : (w.n0 > 0 ? 1 : 0) + (w.n1 > 0 ? 2 : 0);  // bits
                 // Q is read once and comes from far: on its way to L2 before its
                 // place is free
                 if (lane < 2 * G::SLABS && ((tiles_q >> (lane & 1)) & 1))
-                    tma_prefetch_3d(&tm_q, (lane >> 1) * 64, w.head * P.group,
-                                    w.q_tok + (lane & 1) * P.tile_tokens);
+                    tma_prefetch_3d(&tm_q, (lane >> 1) * 64, (w.head + (lane & twin)) * P.group,
+                                    w.q_tok + (lane & 1 & ~twin) * P.tile_tokens);
                 __syncwarp();
                 // in the order of use: K0 V0 K1 V1 ..., with two slots of S
                 // K0 K1 V0 K2 V1 ...; Q behind the first two, whose places are free
@@ -686,16 +712,16 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         mbar_arrive_expect_tx(&bars.kv_full[st], G::TILE);
                         for (int sl = 0; sl < G::SLABS; ++sl)
                             tma_load_3d(sKV + st * G::TILE + sl * G::KV_SLAB, is_k ? &tm_k : &tm_v,
-                                        &bars.kv_full[st], sl * 64, w.head,
-                                        w.k_row + (w.lo + kt) * KEYS);
+                                        &bars.kv_full[st], sl * 64, twin ? w.head + kt : w.head,
+                                        w.k_row + (twin ? 0 : w.lo + kt) * KEYS);
                     }
                     ++g;
                     if (j == 1) {
                         if (ALT) {
-                            load_q(it++ & 1, 0);
+                            load_q(it++ & 1, 0, w.head);
                         } else {
-                            if (tiles_q & 1) load_q(0, 0);
-                            if (ok && (tiles_q & 2)) load_q(1, P.tile_tokens);
+                            if (tiles_q & 1) load_q(0, 0, w.head);
+                            if (ok && (tiles_q & 2)) load_q(1, twin ? 0 : P.tile_tokens, w.head + twin);
                         }
                     }
                 }
@@ -790,10 +816,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mma_commit(full);
                 }
             };
-            const auto pv = [&](int left, bool first) {  // O (+)= P V; left: keys of the tile
+            // O (+)= P V; left: keys of the tile; turn: the two warps' P V in turn
+            const auto pv = [&](int left, bool first, bool turn) {
                 const uint32_t b = (aKV + st * (G::TILE >> 4)) | kLboV;
                 const uint32_t acc = first ? 0u : 1u;
-                if (!ALT) take_turn();
+                if (turn) take_turn();
                 if (first) wait(&bars.o_empty[x], (no & 1) ^ 1, kStatusTimeoutSync);
                 if (!wait(&bars.p_full[x][SLOTS == 2 ? np & 1 : 0], (SLOTS == 2 ? np >> 1 : np) & 1,
                           kStatusTimeoutSync))
@@ -836,32 +863,36 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     ++it;
                 }
                 if constexpr (!ALT) {
-                    // the first S; then per key tile: P V, and S in the slot it frees
+                    // the first S; then per key tile: P V, and S in the slot it frees.
+                    // Twins share no key tile and wait for nothing of each other.
+                    const bool twin = TWINS && __shfl_sync(~0u, w.twin, 0) != 0;
+                    const int end = twin ? x : nx - 1;  // this tile's last
+                    const auto uses = [&](int j) { return twin ? j == x : j < nx; };
                     for (int j = 0; j < SLOTS && j < n; ++j) {
                         if (!kv_wait()) break;
                         tc_fence_after();
-                        if (j < nx) qk(false);
-                        kv_done(j < nx);
+                        if (uses(j)) qk(false);
+                        kv_done(uses(j));
                     }
                     if (!ok) break;
-                    if (nx > 0 && nx <= SLOTS) q_done();
+                    if (nx > 0 && end < SLOTS) q_done();
                     for (int j = 0; j < n; ++j) {
-                        const bool more = j + SLOTS < n, mine = j + SLOTS < nx;
+                        const bool more = j + SLOTS < n, mine = more && uses(j + SLOTS);
                         if (!kv_wait()) break;
                         if (more) kv_peek();
-                        if (j < nx)
-                            pv(keys - j * KEYS, j == 0);
-                        else
+                        if (uses(j))
+                            pv(twin ? keys : keys - j * KEYS, twin || j == 0, !twin);
+                        else if (!twin)
                             take_turn();
                         if (!ok) break;
-                        kv_done(j < nx);
+                        kv_done(uses(j));
                         if (mine)
-                            qk(true);
-                        else
+                            qk(!twin);
+                        else if (!twin)
                             pass_turn();
                         if (more) kv_done(mine);
-                        if (j + SLOTS + 1 == nx) q_done();
-                        if (j + 1 == nx) ++no;
+                        if (mine && j + SLOTS == end) q_done();
+                        if (uses(j) && j == end) ++no;
                     }
                 } else {
                     // this warp's key tiles are x, x + 2, ...; it lets go of the
@@ -874,7 +905,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         kv_done(mine);
                         if (mine && j + 2 >= n) q_done();
                         if (!kv_wait()) break;
-                        if (mine) pv(keys - j * KEYS, j < 2);
+                        if (mine) pv(keys - j * KEYS, j < 2, false);
                         if (!ok) break;
                         kv_done(mine);
                         if (mine && j + 2 >= n) ++no;
@@ -997,7 +1028,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (!more) break;
             const int n = ALT ? (w.n + 1 - x) / 2 : (x ? w.n1 : w.n0);
-            const int shift_tok = ALT ? 0 : x * P.tile_tokens;
+            const int twin = TWINS ? w.twin : 0;
+            const int shift_tok = ALT || twin ? 0 : x * P.tile_tokens;
             const int toks = min(w.toks - shift_tok, P.tile_tokens);  // of this tile
             const bool valid = tok < toks;
             const int lim = P.causal ? min(w.nk, w.lim0 + shift_tok + tok) : w.nk;
@@ -1019,7 +1051,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // having given S, and the one after waits for this P V, so the
                     // parity is unambiguous. Both tiles may do this: they write the
                     // same.)
-                    const int idx = g + 2 * w.n - 1;
+                    const int idx = g + (twin ? (SLOTS == 1 ? 2 * x + 1 : 2 + x) : 2 * w.n - 1);
                     const int st = idx % G::STAGES, use = idx / G::STAGES;
                     ok = __all_sync(~0u, pa_wait_in(&bars.kv_full[st], use & 1, kStatusTimeoutLoad, wc));
                     if (!ok) break;
@@ -1131,7 +1163,7 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 due.m = m;
                 due.l = l;
                 due.token = w.q_tok + shift_tok + tok;
-                due.head = w.head;
+                due.head = w.head + (twin ? x : 0);
                 due.slot = w.slot;
                 is_due = true;
             } else if (PIECES && valid && row < P.ws_rows) {
@@ -1294,7 +1326,7 @@ cudaError_t pa_launch_kind(const PackedAttnMaps &m, const PackedAttnArgs &a, int
                                            PaGeo<D>::SMEM);
     if (err != cudaSuccess) return err;
     err = launch_pdl(kernel, dim3(ctas), dim3(kPaThreads), PaGeo<D>::SMEM, stream, m.q, m.k, m.v, a);
-    if constexpr (KIND != kWhole) {
+    if constexpr (KIND == kShared || KIND == kAlternate) {
         if (err != cudaSuccess) return err;
         constexpr bool ALT = KIND == kAlternate;
         const int64_t rows = static_cast<int64_t>(a.total_q) * a.group * a.heads_kv;
@@ -1312,6 +1344,7 @@ template <typename T, int D>
 cudaError_t pa_launch(const PackedAttnMaps &m, const PackedAttnArgs &a, int kind, int ctas,
                       cudaStream_t stream) {
     return kind == kWhole    ? pa_launch_kind<T, D, kWhole>(m, a, ctas, stream)
+           : kind == kTwins  ? pa_launch_kind<T, D, kTwins>(m, a, ctas, stream)
            : kind == kShared ? pa_launch_kind<T, D, kShared>(m, a, ctas, stream)
                              : pa_launch_kind<T, D, kAlternate>(m, a, ctas, stream);
 }

@@ -178,7 +178,7 @@ struct PackedAttnArgs {
     void *out;
     int64_t out_token, out_head;
     float *lse;  // [total_q, heads_q] or NULL
-    // pieces: the workspace (a header, two int4 per item), each token's first
+    // pieces: the workspace (a header, an int4 per item), each token's first
     // item, the row references and sums, the unnormalised outputs
     // [slot][2][ws_rows][D]
     void *workspace;
@@ -191,7 +191,7 @@ struct PackedAttnArgs {
 struct PackedAttnMaps {
     CUtensorMap q, k, v;
 };
-// kind: 0 whole items on `ctas` CTAs; 1, 2 (two tiles that share their keys,
+// kind: 0, 3 whole items on `ctas` CTAs (3: short ones by two heads); 1, 2 (two tiles that share their keys,
 // one tile with its keys dealt over the warpgroups): the kernel that writes
 // unnormalised pieces, then the one that joins them. bf16: the type.
 cudaError_t launch_packed_attn_d64(const PackedAttnMaps &m, const PackedAttnArgs &a, bool bf16,
