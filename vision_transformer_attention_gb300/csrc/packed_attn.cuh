@@ -1184,11 +1184,11 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 // Its time is that of its chain of reads (the row's item, the item's pieces,
 // then (m, l) and O together), so nothing is divided between them, the first O
 // vectors are under way before their factors are known, and half a warp takes a
-// row where rows are many. WIDE: a CTA per row, its warps taking every eighth
+// row where rows are many. WIDE: a CTA per row, its warps taking every 16th
 // piece (few rows, many pieces). Rows of no sequence are left alone: their entry
 // of ws_item is whatever the workspace held, which is believed only if the item
 // it names says that it holds the row.
-constexpr int kJoinWarps = 8;
+constexpr int join_warps(bool wide) { return wide ? 16 : 4; }
 
 template <int N>
 __device__ __forceinline__ float join_max(float v) {
@@ -1205,16 +1205,16 @@ __device__ __forceinline__ float join_sum(float v) {
 }
 
 template <typename T, int D, bool ALT, bool WIDE>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(32 * join_warps(WIDE))
 packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int ctas) {
     constexpr int LANES = WIDE ? 32 : 16;             // of a row
     constexpr int W = D / LANES < 4 ? D / LANES : 4;  // floats of a vector
     constexpr int N = D / LANES / W;                  // vectors of a lane, LANES * W apart
-    constexpr int STEP = WIDE ? kJoinWarps : 1, U = 4;
-    __shared__ float part[WIDE ? kJoinWarps : 1][WIDE ? D : 1];
+    constexpr int WARPS = join_warps(WIDE), STEP = WIDE ? WARPS : 1, U = WIDE ? 2 : 4;
+    __shared__ float part[WIDE ? WARPS : 1][WIDE ? D : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LANES - 1);
     const int heads = P.group * P.heads_kv, rows = P.total_q * heads;  // below 2^31
-    const int want = WIDE ? blockIdx.x : blockIdx.x * (2 * kJoinWarps) + threadIdx.x / LANES;
+    const int want = WIDE ? blockIdx.x : blockIdx.x * (2 * WARPS) + threadIdx.x / LANES;
     const int out_row = min(want, rows - 1);
     const int token = out_row / heads;
     const int out_head = out_row - token * heads, kv_head = out_head / P.group;
@@ -1293,7 +1293,7 @@ packed_combine_kernel(const __grid_constant__ PackedAttnArgs P, int ctas) {
             for (int e = 0; e < W; ++e) {
                 float s = 0.f;
 #pragma unroll
-                for (int i = 0; i < kJoinWarps; ++i) s += part[i][(n * LANES + lane) * W + e];
+                for (int i = 0; i < WARPS; ++i) s += part[i][(n * LANES + lane) * W + e];
                 acc[n][e] = s;
             }
     }
@@ -1332,10 +1332,10 @@ cudaError_t pa_launch_kind(const PackedAttnMaps &m, const PackedAttnArgs &a, int
         const int64_t rows = static_cast<int64_t>(a.total_q) * a.group * a.heads_kv;
         if (rows <= 4 * sm_count())
             return launch_pdl(packed_combine_kernel<T, D, ALT, true>, dim3(static_cast<unsigned>(rows)),
-                              dim3(32 * kJoinWarps), 0, stream, a, ctas);
+                              dim3(32 * join_warps(true)), 0, stream, a, ctas);
         return launch_pdl(packed_combine_kernel<T, D, ALT, false>,
-                          dim3(static_cast<unsigned>((rows + 2 * kJoinWarps - 1) / (2 * kJoinWarps))),
-                          dim3(32 * kJoinWarps), 0, stream, a, ctas);
+                          dim3(static_cast<unsigned>((rows + 2 * join_warps(false) - 1) / (2 * join_warps(false)))),
+                          dim3(32 * join_warps(false)), 0, stream, a, ctas);
     }
     return err;
 }
