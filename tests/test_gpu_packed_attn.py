@@ -1,7 +1,7 @@
 """Attention over packed sequences (packed_attn_fwd) against the definition in
 64 bits.
 
-Error budget of an output with W = sum_j softmax_j |v_j| (u: half a step of the
+Error allowed of an output with W = sum_j softmax_j |v_j| (u: half a step of the
 type, finfo.eps / 2): the probabilities' rounding u W, the output's u |out|,
 and e W twice (numerator and denominator) for the relative error e of a
 probability in fp32: 2^-22 of the exponential, the exponent's rounding (2^-23

@@ -1,7 +1,7 @@
 """Rotary positions and per-head norms (rope_build_phases, rope_fwd,
 qk_norm_rope_fwd) against the formulas in 64 bits.
 
-Error budget of one output y of a pair (x1, x2) with h = |m| hypot(x1, x2)
+Error allowed of one output y of a pair (x1, x2) with h = |m| hypot(x1, x2)
 (after the norm, if there is one): the angle's fraction of a turn is exact but
 for its rounding to 24 bits (pi 2^-25), sincospi is good to 2 ulp (2^-23), the
 two products, their sum and the magnitude round 2^-24 each: under 2^-21 h. A

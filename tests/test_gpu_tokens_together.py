@@ -1,7 +1,7 @@
 """The calls on tokens as a program uses them, one after another: a projection's queries and keys
 normed and turned in place or into a cache, attention over them, prompts and then single tokens,
 captured steps, and the patch grid's attention behind the rotation. Each stage is held to its own
-budget on the tensors that it read (test_gpu_rope, test_gpu_packed_attn). And what both kinds of
+tolerance on the tensors that it read (test_gpu_rope, test_gpu_packed_attn). And what both kinds of
 call share: the quick way into the library against the checked one, and offsets past 2^31.
 """
 import random

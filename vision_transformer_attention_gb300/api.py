@@ -393,7 +393,8 @@ def packed_attn_fwd(q, k, v, cu_q, cu_k=None, k_lens=None, causal=False, scale=N
 
 def rpe_device_status(clear=True):
     """Synchronises the device; returns the device status word (0 = none; bits
-    0-4 a bounded wait ran out, bit 5 an offset table held an id out of range)."""
+    0-4 a bounded wait ran out, bit 5 an offset table held an id out of range, bit 6
+    packed sequences overlapped or left their tensors)."""
     st = ctypes.c_uint(0)
     rc = _lib.lib().rpe_device_status(ctypes.byref(st), int(bool(clear)))
     if rc not in (_lib.RPE_OK, _lib.RPE_ERR_TIMEOUT, _lib.RPE_ERR_INVALID_ARG) or (

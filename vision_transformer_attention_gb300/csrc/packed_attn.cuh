@@ -936,7 +936,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // none after it can be: the phase is unambiguous.)
         const auto pv_over = [&]() {
             const int k = ns - 1;
-            return __all_sync(~0u, pa_wait_in(&bars.pv_done[x][SLOTS == 2 ? k & 1 : 0], (SLOTS == 2 ? k >> 1 : k) & 1, kStatusTimeoutMma, wc));
+            return __all_sync(~0u, pa_wait_in(&bars.pv_done[x][SLOTS == 2 ? k & 1 : 0],
+                                              (SLOTS == 2 ? k >> 1 : k) & 1, kStatusTimeoutMma, wc));
         };
         // What is to be written of the item before: its rows are written once the
         // last P V is complete, which the next item's first S comes behind; O is
@@ -1042,7 +1043,8 @@ packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int i = 0; i < n; ++i, ++ns) {
                 const int j = ALT ? 2 * i + x : i, kt = w.lo + j;
                 const int sl = SLOTS == 2 ? ns & 1 : 0;
-                ok = __all_sync(~0u, pa_wait_in(&bars.s_full[x][sl], (SLOTS == 2 ? ns >> 1 : ns) & 1, kStatusTimeoutMma, wc));
+                ok = __all_sync(~0u, pa_wait_in(&bars.s_full[x][sl], (SLOTS == 2 ? ns >> 1 : ns) & 1,
+                                                kStatusTimeoutMma, wc));
                 if (!ok) break;
                 if (w.nk < (kt + 1) * KEYS) {
                     // A part tile (the item's last): V's rows behind the sequence in
