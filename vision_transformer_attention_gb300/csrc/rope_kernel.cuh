@@ -629,10 +629,13 @@ cudaError_t rope_launch_run(RopeArgs A, cudaStream_t stream) {
     const int HP = 32 / A.lanes, heads = A.heads[0] + A.heads[1], pairs = A.rotary / 2;
     const int64_t rows = A.units * heads;
     const int64_t most = static_cast<int64_t>(rope_ctas_per_sm(norm)) * sm_count();
-    // A run is as many passes as leave two runs per warp, 16 at most, and has no
-    // more tokens than 1024 pairs of angles (8 KB per warp) serve.
-    int64_t passes = rows / (2 * most * kRopeWarps * HP);
-    passes = passes < 1 ? 1 : passes > 16 ? 16 : passes;
+    // Runs of as many passes as make one run per warp with norms, three without
+    // (12 heads of 64: 22.1 us with one, 23.4 with three; without norms, fp32, 20.3
+    // and 18.6), of 16 passes at most, and of no more tokens than 1024 pairs of
+    // angles (8 KB per warp) serve.
+    const int64_t round = (norm ? 1 : 3) * most * kRopeWarps * HP;
+    int64_t passes = (rows + round - 1) / round;
+    passes = passes > 16 ? 16 : passes;
     const auto tokens_of = [&](int64_t p) { return static_cast<int>((p * HP + heads - 2) / heads + 1); };
     while (passes > 1 && tokens_of(passes) * pairs > 1024) --passes;
     A.run_rows = static_cast<int>(passes * HP);
@@ -657,7 +660,7 @@ cudaError_t rope_launch_run(RopeArgs A, cudaStream_t stream) {
 
 // 16-byte vectors throughout: by token where its heads fill four passes or more
 // (40 heads of 128: 56 us by token, 70 in runs), else in runs (12 heads of 64: 32
-// and 24 us).
+// and 22 us).
 template <typename T>
 cudaError_t rope_launch_wide(const RopeArgs &A, cudaStream_t stream) {
     constexpr int E = Wide<T>::E;
