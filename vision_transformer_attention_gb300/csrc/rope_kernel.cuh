@@ -231,22 +231,6 @@ rope_token_kernel(const __grid_constant__ RopeArgs A) {
     };
 
     griddep_wait();
-    if constexpr (NORM) {
-        for (int i = threadIdx.x; i < 2 * A.d; i += 32 * kRopeWarps) {
-            const int role = i >= A.d ? 1 : 0, e = i - role * A.d;
-            const void *g = A.gain[role];
-            // channels past d would be read by lanes without a second vector
-            gain_s[role * (A.d + E) + e] =
-                g == nullptr ? 1.f
-                             : (A.gain_f32 ? static_cast<const float *>(g)[e]
-                                           : to_f32(static_cast<const T *>(g)[e]));
-        }
-        if (threadIdx.x < 2 * E)
-            gain_s[(threadIdx.x >= E ? A.d + E : 0) + A.d + threadIdx.x % E] = 0.f;
-        __syncthreads();
-    }
-    if (item0 >= items) return;
-
     Walk in, out;
     start(in, A.src);
     start(out, A.dst);
@@ -262,6 +246,22 @@ rope_token_kernel(const __grid_constant__ RopeArgs A) {
     };
 #pragma unroll
     for (int s = 0; s < kRopeStages - 1; ++s) ask(s);
+    // the gains behind the first passes, so that the two reads' latencies overlap
+    if constexpr (NORM) {
+        for (int i = threadIdx.x; i < 2 * A.d; i += 32 * kRopeWarps) {
+            const int role = i >= A.d ? 1 : 0, e = i - role * A.d;
+            const void *g = A.gain[role];
+            // channels past d would be read by lanes without a second vector
+            gain_s[role * (A.d + E) + e] =
+                g == nullptr ? 1.f
+                             : (A.gain_f32 ? static_cast<const float *>(g)[e]
+                                           : to_f32(static_cast<const T *>(g)[e]));
+        }
+        if (threadIdx.x < 2 * E)
+            gain_s[(threadIdx.x >= E ? A.d + E : 0) + A.d + threadIdx.x % E] = 0.f;
+        __syncthreads();
+    }
+    if (item0 >= items) return;
 
     // (c, s, n = -s) of this lane's pairs, two pairs to a float2
     const auto turn = [&](float2 v1, float2 v2, float2 c, float2 s, float2 n, float2 &y1,
@@ -475,19 +475,6 @@ rope_run_kernel(const __grid_constant__ RopeArgs A) {
     };
 
     griddep_wait();
-    if constexpr (NORM) {
-        for (int i = threadIdx.x; i < 2 * gain_row; i += 32 * kRopeWarps) {
-            const int role = i >= gain_row ? 1 : 0, e = i - role * gain_row;
-            const void *g = A.gain[role];
-            gain_s[i] = e >= A.d       ? 0.f
-                        : g == nullptr ? 1.f
-                                       : (A.gain_f32 ? static_cast<const float *>(g)[e]
-                                                     : to_f32(static_cast<const T *>(g)[e]));
-        }
-        __syncthreads();
-    }
-    if (run0 >= runs) return;
-
     Run in, out;
     enter(in, run0);
     int in_row = group;  // of the run `in`, the next to be asked for
@@ -509,6 +496,18 @@ rope_run_kernel(const __grid_constant__ RopeArgs A) {
     };
 #pragma unroll
     for (int s = 0; s < kRopeStages - 1; ++s) ask(s);
+    if constexpr (NORM) {
+        for (int i = threadIdx.x; i < 2 * gain_row; i += 32 * kRopeWarps) {
+            const int role = i >= gain_row ? 1 : 0, e = i - role * gain_row;
+            const void *g = A.gain[role];
+            gain_s[i] = e >= A.d       ? 0.f
+                        : g == nullptr ? 1.f
+                                       : (A.gain_f32 ? static_cast<const float *>(g)[e]
+                                                     : to_f32(static_cast<const T *>(g)[e]));
+        }
+        __syncthreads();
+    }
+    if (run0 >= runs) return;
 
     const auto turn = [&](float2 v1, float2 v2, float2 c, float2 s, float2 &y1, float2 &y2) {
         y1 = ffma2(v2, make_float2(-s.x, -s.y), fmul2(v1, c));
